@@ -106,10 +106,8 @@ struct tb_ctx {
     std::string err;
 };
 
-namespace {
+namespace tb {
 
-// Records a message on ctx and returns code.
-int fail(tb_ctx *ctx, int code, const char *fmt, ...) __attribute__((format(printf, 3, 4)));
 int fail(tb_ctx *ctx, int code, const char *fmt, ...)
 {
     if (ctx) {
@@ -128,34 +126,35 @@ int cuda_fail(tb_ctx *ctx, cudaError_t e, const char *what)
     return fail(ctx, TB_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
+int ctx_device(const tb_ctx *ctx)
+{
+    return ctx->device;
+}
+
+int ctx_num_sms(const tb_ctx *ctx)
+{
+    return ctx->num_sms;
+}
+
+const tb_options &ctx_options(const tb_ctx *ctx)
+{
+    return ctx->opt;
+}
+
+}  // namespace tb
+
+using tb::cuda_fail;
+using tb::DeviceScope;
+using tb::fail;
+
+namespace {
+
 #define TB_CUDA(ctx, call)                                   \
     do {                                                     \
         cudaError_t e_ = (call);                             \
         if (e_ != cudaSuccess)                               \
             return cuda_fail((ctx), e_, #call);              \
     } while (0)
-
-// Makes ctx's device current for the scope and restores the caller's after.
-class DeviceScope {
-  public:
-    explicit DeviceScope(int device)
-    {
-        if (cudaGetDevice(&prev_) == cudaSuccess && prev_ != device)
-            ok_ = cudaSetDevice(device) == cudaSuccess;
-        else
-            prev_ = -1;
-    }
-    ~DeviceScope()
-    {
-        if (prev_ >= 0)
-            cudaSetDevice(prev_);
-    }
-    bool ok() const { return ok_; }
-
-  private:
-    int prev_ = -1;
-    bool ok_ = true;
-};
 
 bool env_u64(const char *name, uint64_t *out, bool *bad)
 {

@@ -11,6 +11,38 @@
 namespace tb {
 
 // ---------------------------------------------------------------------------
+// What the host files share of a context (tb_host.cpp)
+// ---------------------------------------------------------------------------
+// Records a message on ctx and returns code.
+int fail(tb_ctx *ctx, int code, const char *fmt, ...) __attribute__((format(printf, 3, 4)));
+int cuda_fail(tb_ctx *ctx, cudaError_t e, const char *what);
+int ctx_device(const tb_ctx *ctx);
+int ctx_num_sms(const tb_ctx *ctx);
+const tb_options &ctx_options(const tb_ctx *ctx);
+
+// Makes a device current for the scope and restores the caller's after.
+class DeviceScope {
+  public:
+    explicit DeviceScope(int device)
+    {
+        if (cudaGetDevice(&prev_) == cudaSuccess && prev_ != device)
+            ok_ = cudaSetDevice(device) == cudaSuccess;
+        else
+            prev_ = -1;
+    }
+    ~DeviceScope()
+    {
+        if (prev_ >= 0)
+            cudaSetDevice(prev_);
+    }
+    bool ok() const { return ok_; }
+
+  private:
+    int prev_ = -1;
+    bool ok_ = true;
+};
+
+// ---------------------------------------------------------------------------
 // Reduce-copy (K1)
 // ---------------------------------------------------------------------------
 

@@ -161,6 +161,55 @@ class BatchStats(ct.Structure):
     ]
 
 
+class KvCacheStruct(ct.Structure):
+    """tb_kv_cache: see include/tb.h."""
+    _fields_ = [
+        ("k", _vp),
+        ("v", _vp),
+        ("table", _vp),
+        ("held", _vp),
+        ("lens", _vp),
+        ("refs", _vp),
+        ("dtype", _i32),
+        ("layers", _i32),
+        ("pages", _i32),
+        ("page_tokens", _i32),
+        ("kv_heads", _i32),
+        ("head_dim", _i32),
+        ("slots", _i32),
+        ("table_width", _i32),
+        ("layer_stride", _i64),
+        ("page_stride", _i64),
+        ("token_stride", _i64),
+        ("head_stride", _i64),
+    ]
+
+
+class Tree(ct.Structure):
+    """tb_tree: see include/tb.h."""
+    _fields_ = [
+        ("cache", ct.POINTER(KvCacheStruct)),
+        ("layer", _i32),
+        ("seqs", _i32),
+        ("seq_slots", _vp),
+        ("q_start", _vp),
+        ("rows", _i32),
+        ("q_heads", _i32),
+        ("scale", ct.c_float),
+        ("q", _vp),
+        ("out", _vp),
+        ("q_row_stride", _i64),
+        ("q_head_stride", _i64),
+        ("out_row_stride", _i64),
+        ("out_head_stride", _i64),
+        ("lse", _vp),
+        ("mask", _vp),
+        ("mask_words", _i32),
+        ("workspace", _vp),
+        ("workspace_bytes", _u64),
+    ]
+
+
 class Mismatch(ct.Structure):
     _fields_ = [("index", _i64), ("expected", _u32), ("actual", _u32)]
 
@@ -201,6 +250,13 @@ _sig("tb_copy_each", ct.c_int, _vp, _vp, ct.c_size_t, _vp)  # desc: a CopyDesc a
 _sig("tb_validate", ct.c_int, _vp, _vp, _vp, _u64, _u32, _P(Mismatch))
 _sig("tb_validate_device", ct.c_int, _vp, _vp, _vp, _u64, _u32, _P(Mismatch))
 _sig("tb_batch_copy_noalloc", ct.c_int, _vp, ct.c_size_t, _vp)  # desc: as tb_batch_copy
+_KV = _P(KvCacheStruct)
+_sig("tb_kv_copy_pages", ct.c_int, _vp, _KV, _vp, _vp, _vp, _i32, _vp)
+_sig("tb_kv_resize", ct.c_int, _vp, _KV, _vp, _vp, _vp)
+_sig("tb_kv_fork", ct.c_int, _vp, _KV, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("tb_kv_compact", ct.c_int, _vp, _KV, _vp, _vp, _i32, _vp, _vp, _vp)
+_sig("tb_tree_attention", ct.c_int, _vp, _P(Tree), _vp)
+_sig("tb_tree_attention_workspace", ct.c_int, _vp, _KV, _i32, _P(_u64))
 
 TB_NOALLOC_MAX_ITEMS = 65536
 TB_EXEC_GPU = 0
@@ -311,6 +367,109 @@ def repeat_pattern(values) -> tuple[Pattern, object]:
     p = Pattern(kind=TB_PATTERN_REPEAT, repeat=ct.cast(buf, ct.POINTER(ct.c_float)),
                 repeat_len=len(values))
     return p, buf  # keep buf alive for the call
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache
+# ---------------------------------------------------------------------------
+TB_DTYPE_F16 = 0
+TB_DTYPE_BF16 = 1
+TB_DTYPE_F32 = 2
+TB_DTYPE_BYTE = 3
+TB_KV_MAX_SLOTS = 8192
+TB_TREE_MAX_SEQS = 4096
+
+
+def _dtype_name(t) -> str:
+    return str(t.dtype).replace("torch.", "")
+
+
+def _kv_dtype(t) -> int:
+    name = _dtype_name(t)
+    known = {"float16": TB_DTYPE_F16, "bfloat16": TB_DTYPE_BF16, "float32": TB_DTYPE_F32}
+    if name in known:
+        return known[name]
+    if t.element_size() == 1:
+        return TB_DTYPE_BYTE
+    raise TypeError(f"no cache of {name}")
+
+
+def _int32(t, what: str, *shape: int | None):
+    """Checks a dense int32 device tensor's shape (None: any size)."""
+    if t is None or _dtype_name(t) != "int32" or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous int32 CUDA tensor")
+    if len(t.shape) != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    return t
+
+
+class KvCache:
+    """A tb_kv_cache with the tensors it points into (see kv_cache)."""
+
+    def __init__(self, struct: KvCacheStruct, tensors: tuple):
+        self.struct = struct
+        self.ref = ct.byref(struct)
+        self.tensors = tensors
+        self.name = _dtype_name(tensors[0]) if tensors[0] is not None else ""
+
+
+def kv_cache(k=None, v=None, table=None, held=None, lens=None, refs=None, layout: str = "NHD",
+             page_tokens: int | None = None) -> KvCache:
+    """Describes a paged key/value cache held in CUDA tensors (tb_kv_cache).
+
+    k, v: [layers, pages, page_tokens, heads, dim] for layout "NHD" or
+    [layers, pages, heads, page_tokens, dim] for "HND", of any strides with
+    dense dim.  table: int32 [slots, width]; held, lens: int32 [slots]; refs:
+    int32 [pages].  A cache described without k and v (page_tokens given
+    instead) serves kv_resize, one without the table kv_copy_pages.  The
+    description holds addresses: describe the cache again when a tensor is
+    replaced.
+    """
+    if layout not in ("NHD", "HND"):
+        raise ValueError(f"layout {layout!r} is neither NHD nor HND")
+    s = KvCacheStruct(dtype=TB_DTYPE_BYTE)
+    if (k is None) != (v is None):
+        raise ValueError("k and v come together")
+    if k is not None:
+        if not k.is_cuda or not v.is_cuda or k.dim() != 5 or k.shape != v.shape \
+                or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be 5-d CUDA tensors of one shape, type and strides")
+        if k.shape[4] > 1 and k.stride(4) != 1:
+            raise ValueError("the last dimension of k and v must be dense")
+        e, tokens, heads = k.element_size(), *((2, 3) if layout == "NHD" else (3, 2))
+        if page_tokens is not None and page_tokens != k.shape[tokens]:
+            raise ValueError(f"page_tokens is {page_tokens}, the pools have {k.shape[tokens]}")
+        s.k, s.v, s.dtype = k.data_ptr(), v.data_ptr(), _kv_dtype(k)
+        s.layers, s.pages, s.head_dim = k.shape[0], k.shape[1], k.shape[4]
+        s.page_tokens, s.kv_heads = k.shape[tokens], k.shape[heads]
+        s.layer_stride, s.page_stride = k.stride(0) * e, k.stride(1) * e
+        s.token_stride, s.head_stride = k.stride(tokens) * e, k.stride(heads) * e
+    else:
+        s.page_tokens = page_tokens or 0
+    if table is not None:
+        _int32(table, "table", None, None)
+        s.slots, s.table_width = table.shape
+        _int32(held, "held", s.slots)
+        _int32(lens, "lens", s.slots)
+        _int32(refs, "refs", s.pages if k is not None else None)
+        s.pages = refs.shape[0]
+        s.table, s.held, s.lens, s.refs = (t.data_ptr() for t in (table, held, lens, refs))
+    return KvCache(s, (k, v, table, held, lens, refs))
+
+
+def tree_mask(parents) -> list[list[int]]:
+    """Mask rows of one draft tree for tree_attention: for each drafted token
+    the words whose bits name the token itself and its ancestors.  parents[i]
+    is the index of token i's parent, smaller than i, or negative for a child
+    of the last committed token.  Words are signed, as int32 tensors hold them."""
+    words = (len(parents) + 31) // 32
+    seen: list[int] = []
+    for i, parent in enumerate(parents):
+        if parent >= i:
+            raise ValueError(f"token {i} comes before its parent {parent}")
+        seen.append((seen[parent] if parent >= 0 else 0) | 1 << i)
+    rows = [[bits >> 32 * w & 0xFFFFFFFF for w in range(words)] for bits in seen]
+    return [[w - (1 << 32) if w >> 31 else w for w in row] for row in rows]
 
 
 class Context:
@@ -464,6 +623,93 @@ class Context:
         s = BatchStats()
         self._ok(lib.tb_last_batch_stats(self._h, ct.byref(s)), "tb_last_batch_stats")
         return {name: getattr(s, name) for name, _ in BatchStats._fields_}
+
+    # -- paged key/value cache ---------------------------------------------
+    def kv_copy_pages(self, cache: KvCache, src, dst, n: int | None = None, tokens=None,
+                      stream=None):
+        """tb_kv_copy_pages: page src[i] to page dst[i] in every layer, keys
+        and values, for the first n entries of the lists (default: all)."""
+        _int32(src, "src", None)
+        _int32(dst, "dst", None)
+        most = min(src.shape[0], dst.shape[0])
+        if tokens is not None:
+            most = min(most, _int32(tokens, "tokens", None).shape[0])
+        if n is None:
+            n = most
+        elif n > most:
+            raise ValueError(f"n is {n}, the shortest list has {most} entries")
+        self._ok(lib.tb_kv_copy_pages(self._h, cache.ref, src.data_ptr(), dst.data_ptr(),
+                                      addr(tokens), n, stream_handle(stream)), "tb_kv_copy_pages")
+
+    def kv_resize(self, cache: KvCache, capacity, status, stream=None):
+        """tb_kv_resize: each slot gets exactly the pages of capacity[s] tokens."""
+        _int32(capacity, "capacity", cache.struct.slots)
+        _int32(status, "status", 1)
+        self._ok(lib.tb_kv_resize(self._h, cache.ref, capacity.data_ptr(), status.data_ptr(),
+                                  stream_handle(stream)), "tb_kv_resize")
+
+    def kv_fork(self, cache: KvCache, parents, table_out, held_out, lens_out, status, stream=None):
+        """tb_kv_fork: slot s becomes the sequence of slot parents[s]."""
+        slots = cache.struct.slots
+        _int32(parents, "parents", slots)
+        _int32(table_out, "table_out", slots, cache.struct.table_width)
+        _int32(held_out, "held_out", slots)
+        _int32(lens_out, "lens_out", slots)
+        _int32(status, "status", 1)
+        self._ok(lib.tb_kv_fork(self._h, cache.ref, parents.data_ptr(), table_out.data_ptr(),
+                                held_out.data_ptr(), lens_out.data_ptr(), status.data_ptr(),
+                                stream_handle(stream)), "tb_kv_fork")
+
+    def kv_compact(self, cache: KvCache, start, keep, count, status, stream=None):
+        """tb_kv_compact: token start[s] + keep[s, i] moves to start[s] + i."""
+        slots = cache.struct.slots
+        _int32(start, "start", slots)
+        _int32(keep, "keep", slots, None)
+        _int32(count, "count", slots)
+        _int32(status, "status", slots)
+        self._ok(lib.tb_kv_compact(self._h, cache.ref, start.data_ptr(), keep.data_ptr(),
+                                   keep.shape[1], count.data_ptr(), status.data_ptr(),
+                                   stream_handle(stream)), "tb_kv_compact")
+
+    def tree_attention_workspace(self, cache: KvCache, q_heads: int) -> int:
+        """Bytes of workspace tree_attention needs (tb_tree_attention_workspace)."""
+        n = _u64()
+        self._ok(lib.tb_tree_attention_workspace(self._h, cache.ref, q_heads, ct.byref(n)),
+                 "tb_tree_attention_workspace")
+        return n.value
+
+    def tree_attention(self, cache: KvCache, layer: int, q, q_start, mask, out, workspace,
+                       scale: float | None = None, lse=None, seq_slots=None, stream=None):
+        """tb_tree_attention: q and out [rows, q_heads, dim] of the cache's
+        type, q_start int32 [seqs + 1], mask int32 [rows, words] (bits, see
+        tree_mask), workspace uint8 of tree_attention_workspace bytes; lse
+        float32 [rows, q_heads] when wanted; scale defaults to dim ** -0.5."""
+        s = cache.struct
+        for t, what in ((q, "q"), (out, "out")):
+            if not t.is_cuda or _dtype_name(t) != cache.name or t.dim() != 3 \
+                    or t.shape[2] != s.head_dim or (t.shape[2] > 1 and t.stride(2) != 1):
+                raise ValueError(f"{what} must be a [rows, heads, {s.head_dim}] CUDA tensor of the "
+                                 "cache's type with a dense last dimension")
+        rows, heads, dim = q.shape
+        if out.shape != q.shape:
+            raise ValueError("q and out differ in shape")
+        seqs = _int32(q_start, "q_start", None).shape[0] - 1
+        _int32(mask, "mask", rows, None)
+        if seq_slots is not None:
+            _int32(seq_slots, "seq_slots", seqs)
+        if lse is not None and (_dtype_name(lse) != "float32" or not lse.is_cuda
+                                or not lse.is_contiguous() or tuple(lse.shape) != (rows, heads)):
+            raise ValueError("lse must be a contiguous float32 [rows, q_heads] CUDA tensor")
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        e = q.element_size()
+        t = Tree(ct.pointer(s), layer, seqs, addr(seq_slots), q_start.data_ptr(), rows, heads,
+                 dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
+                 q.stride(0) * e, q.stride(1) * e, out.stride(0) * e, out.stride(1) * e, addr(lse),
+                 mask.data_ptr(), mask.shape[1], workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size())
+        self._ok(lib.tb_tree_attention(self._h, ct.byref(t), stream_handle(stream)),
+                 "tb_tree_attention")
 
     # -- validation --------------------------------------------------------
     def validate_device(self, dst_device, expected_device, num_bytes: int, elem_size: int = 4):

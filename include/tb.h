@@ -2,7 +2,8 @@
  * tb.h - C ABI of libtb, a single-GPU GB300 (sm_103a) reduce-copy and
  * batched-copy engine.
  *
- * Two operations sit on the hot path:
+ * Two operations sit on the hot path, and the paged key/value cache that the
+ * second one's copies serve has its own (section "Paged key/value cache"):
  *
  *  1. The GPU-executor transfer of TransferBench: dst[i] = src0[i] + ... +
  *     srcN-1[i] over float32 buffers, with source-slice rotation so that
@@ -544,6 +545,148 @@ int tb_last_batch_kernel_ms(tb_ctx *ctx, double *ms);
    descriptor with len > 0, in array order, on `stream`.  Same arguments and
    checks as tb_batch_copy; provided so the two can be timed side by side. */
 int tb_copy_each(tb_ctx *ctx, const tb_copy_desc *desc, size_t n, tb_stream stream);
+
+/* ----------------------------------------------------------------------- */
+/* Paged key/value cache                                                    */
+/* ----------------------------------------------------------------------- */
+/* The cache whose pages the batched copies move, as device state: pages of
+   page_tokens tokens, a table that names the pages of each sequence slot, and
+   a count of the table entries that name each page.  Every call below is
+   asynchronous on `stream`, reads its lists from device memory (so no list
+   goes through the host), allocates nothing, and may be captured into a CUDA
+   graph.  Calls that change the table or the counts are to be ordered with
+   one another (one stream, or events).  A page number or a position outside
+   the cache is never dereferenced.
+
+   Invariants the calls keep and rely on: slot s holds pages table[s][0 ..
+   held[s]), entries after them are -1; refs[p] is the number of table entries
+   that name page p, 0 = free; the pages of tokens lens[s] and later are named
+   by slot s alone (a page that a later token is written into is never
+   shared). */
+
+#define TB_DTYPE_F16   0
+#define TB_DTYPE_BF16  1
+#define TB_DTYPE_F32   2  /* page operations only */
+#define TB_DTYPE_BYTE  3  /* any 8-bit format; page operations only */
+
+/* Slots that tb_kv_resize and tb_kv_fork accept at most. */
+#define TB_KV_MAX_SLOTS 8192
+/* Sequences that one tb_tree_attention call accepts at most. */
+#define TB_TREE_MAX_SEQS 4096
+
+typedef struct {
+    /* Element (layer 0, page 0, token 0, head 0, 0) of the two pools; both
+       have the strides below, in bytes, and head_dim contiguous elements.
+       Pointers, strides and head_dim * element size are multiples of 16.  Any
+       order of the four strided dimensions is fine as long as no two elements
+       share an address: tokens before heads, heads before tokens, keys and
+       values interleaved. */
+    void *k, *v;
+    int32_t *table;           /* device [slots][table_width] */
+    int32_t *held;            /* device [slots]: pages the slot holds */
+    int32_t *lens;            /* device [slots]: tokens the slot holds */
+    int32_t *refs;            /* device [pages] */
+    int32_t dtype;            /* TB_DTYPE_* */
+    int32_t layers, pages, page_tokens, kv_heads, head_dim;
+    int32_t slots, table_width;
+    int64_t layer_stride, page_stride, token_stride, head_stride;
+} tb_kv_cache;
+
+/* Copies pages: for i in [0, n), every layer, keys and values, the first
+   tokens[i] tokens (all page_tokens of them when tokens is NULL; clamped to
+   [0, page_tokens]) of page src[i] to page dst[i].  src, dst and tokens are
+   device arrays.  An entry with a page outside [0, pages) is skipped, so
+   lists may be padded with -1.  A page that is both written and read by other
+   entries, or written twice, holds an undefined one of the values.  Bits are
+   copied as they are.  Uses k, v and the sizes of *cache, not its table. */
+int tb_kv_copy_pages(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *src,
+                     const int32_t *dst, const int32_t *tokens, int32_t n, tb_stream stream);
+
+/* Gives each slot exactly the pages of capacity[s] tokens (device [slots]):
+   missing pages are taken, surplus ones given back (refs - 1), entries after
+   the new end become -1; a negative capacity leaves its slot alone and 0
+   frees it.  lens[s] becomes min(lens[s], capacity[s]).  Pages are handed out
+   in slot order, then row order, the lowest free one first, among those free
+   when the call began: the result does not depend on timing.  *status
+   (device) receives 0, the number of pages missing, or -1 when a capacity
+   needs more than table_width pages; unless it is 0 nothing else changes. */
+int tb_kv_resize(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *capacity,
+                 int32_t *status, tb_stream stream);
+
+/* Replaces every slot s by the sequence of slot parents[s] (device [slots];
+   negative: the slot becomes empty, s: it goes on), as a step of a beam search
+   does, without copying full pages.  The new table, held and lens go to the
+   three output arrays (the same shapes, not overlapping cache->table, held,
+   lens; the next call's inputs), the counts and pages change in place.
+   A parent's full pages are shared by all its children.  Its last page, if
+   partly filled, and its pages after that go to one child: the slot itself if
+   it goes on, else the lowest one; each other child takes a fresh page (in
+   slot order, the lowest free one first, among those free when the call
+   began) and the part-filled page's tokens are copied there in every layer.
+   Rows of childless slots are given back.  *status (device) receives 0, the
+   number of pages missing, or -1 when a parent is >= slots; unless it is 0 the
+   outputs are copies of the inputs and nothing else changes. */
+int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
+               int32_t *table_out, int32_t *held_out, int32_t *lens_out, int32_t *status,
+               tb_stream stream);
+
+/* Squeezes kept tokens together: in slot s, for i in [0, count[s]), the token
+   at start[s] + keep[s * keep_stride + i] moves to start[s] + i, in every
+   layer, keys and values, as if in order of i; then lens[s] = start[s] +
+   count[s].  keep ascends strictly.  With start = the committed length and
+   keep = the accepted path of a draft tree this commits that path; with start
+   = 0 it drops the tokens not listed.  Pages past the new length stay with
+   the slot (tb_kv_resize gives them back).  A negative count leaves its slot
+   alone.  status[s] (device [slots]) receives 0; 1 when a token would move
+   into a page that other rows share; 2 when the list does not ascend, count
+   exceeds keep_stride or a position lies outside the slot's pages; a slot
+   with a nonzero status is unchanged. */
+int tb_kv_compact(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *start,
+                  const int32_t *keep, int32_t keep_stride, const int32_t *count,
+                  int32_t *status, tb_stream stream);
+
+typedef struct {
+    const tb_kv_cache *cache; /* TB_DTYPE_F16 or _BF16, head_dim <= 128 */
+    int32_t layer;
+    int32_t seqs;             /* sequences of this call, up to TB_TREE_MAX_SEQS */
+    const int32_t *seq_slots; /* device [seqs]: the slot of each; NULL = 0, 1, 2, ... */
+    const int32_t *q_start;   /* device [seqs + 1]: query rows of sequence b are
+                                 q_start[b] .. q_start[b + 1] - 1, ascending from 0 */
+    int32_t rows;             /* query rows in all, q_start[seqs] */
+    int32_t q_heads;          /* a multiple of kv_heads; head h reads cache head
+                                 h / (q_heads / kv_heads) */
+    float scale;
+    const void *q;            /* [rows][q_heads][head_dim], the cache's type */
+    void *out;                /* the same shape and type */
+    int64_t q_row_stride, q_head_stride;     /* bytes, multiples of 16 */
+    int64_t out_row_stride, out_head_stride;
+    float *lse;               /* NULL, or [rows][q_heads] */
+    const uint32_t *mask;     /* device [rows][mask_words] */
+    int32_t mask_words;       /* drafts past 32 * mask_words are hidden */
+    void *workspace;          /* device, 16-byte aligned */
+    uint64_t workspace_bytes; /* >= tb_tree_attention_workspace */
+} tb_tree;
+
+/* Attention of a tree of drafted tokens over the cache.  Sequence b has n =
+   lens[slot] committed tokens and T = q_start[b + 1] - q_start[b] drafted
+   ones, whose keys and values lie at positions n .. n + T - 1 of its pages.
+   Row i of it sees every committed position, and draft j where bit j % 32 of
+   mask[row][j / 32] is set (for a tree: itself and its ancestors):
+     s_j = scale * q . k_j,  out = sum_j exp(s_j - m) v_j / l,  l = sum_j exp(s_j - m),
+     m = max_j s_j,  lse = m + ln l  (natural logarithm).
+   A row that sees nothing gets out = 0 and lse = -inf.  Hidden positions do
+   not reach the result, whatever their bits.  Sums, maxima and the output
+   accumulate in 32 bits.  The result depends on the inputs alone: two calls
+   give the same bits.  Every position needs a page in the slot's row; what
+   has none reads as zeros. */
+int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream);
+
+/* Bytes of workspace tb_tree_attention needs on this context's device for a
+   cache and a number of query heads, whatever the sequences.  The workspace
+   carries nothing from one call to the next; calls that may overlap need one
+   each. */
+int tb_tree_attention_workspace(tb_ctx *ctx, const tb_kv_cache *cache, int32_t q_heads,
+                                uint64_t *bytes);
 
 /* Non-empty descriptors one tb_batch_copy_noalloc call can take. */
 #define TB_NOALLOC_MAX_ITEMS 65536

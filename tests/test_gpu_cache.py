@@ -1,0 +1,390 @@
+"""The page operations of the paged cache against a plain model: every bit of
+the pools, the table, the counts and the lengths has to be the model's."""
+import numpy as np
+import pytest
+
+from cache_model import CacheModel
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from copy_reduce_dst_gb300 import _build  # noqa: E402
+
+_build.build()
+from copy_reduce_dst_gb300 import tb  # noqa: E402
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32, "byte": torch.uint8}
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    with tb.Context(0) as c:
+        yield c
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Cache:
+    """A cache on the GPU and its model, filled with random bits."""
+
+    def __init__(self, layers=2, pages=24, P=4, heads=2, dim=16, slots=5, width=6, layout="NHD",
+                 dtype="bf16", seed=0):
+        g = np.random.default_rng(seed)
+        self.layout, t = layout, TYPES[dtype]
+        size = torch.empty(0, dtype=t).element_size()
+        shape = (layers, pages, P, heads, dim * size)
+        bits = [g.integers(0, 256, shape, dtype=np.uint8) for _ in "kv"]
+        self.pools = []
+        if layout == "mixed":  # keys and values side by side, pages outermost, gaps after a token
+            self.whole = torch.zeros(pages, layers, P, heads, 2, dim * size + 16, dtype=torch.uint8,
+                                     device="cuda")
+            for i in range(2):
+                view = self.whole[:, :, :, :, i, :dim * size].permute(1, 0, 2, 3, 4)
+                view.copy_(dev(bits[i]))
+                self.pools.append(view.view(t))
+        else:
+            for b in bits:
+                b = dev(b) if layout == "NHD" else dev(b.transpose(0, 1, 3, 2, 4))
+                self.pools.append(b.view(t))
+        self.table = dev(np.full((slots, width), -1, np.int32))
+        self.held, self.lens = (dev(np.zeros(slots, np.int32)) for _ in "hl")
+        self.refs = dev(np.zeros(pages, np.int32))
+        self.status = dev(np.full(1, -7, np.int32))
+        self.model = CacheModel(*bits, *(x.cpu().numpy() for x in (self.table, self.held, self.lens,
+                                                                   self.refs)))
+        self.describe()
+
+    def describe(self):
+        self.c = tb.kv_cache(*self.pools, self.table, self.held, self.lens, self.refs,
+                             layout="HND" if self.layout == "HND" else "NHD")
+
+    def set_lens(self, lens):
+        self.model.lens[:] = lens
+        self.lens.copy_(dev(np.asarray(lens, np.int32)))
+
+    def resize(self, ctx, capacity, stream=None):
+        ctx.kv_resize(self.c, dev(np.asarray(capacity, np.int32)), self.status, stream)
+        return self.model.resize(capacity)
+
+    def fork(self, ctx, parents):
+        out = [torch.full_like(x, 77) for x in (self.table, self.held, self.lens)]
+        ctx.kv_fork(self.c, dev(np.asarray(parents, np.int32)), *out, self.status)
+        self.table, self.held, self.lens = out
+        self.describe()
+        return self.model.fork(parents)
+
+    def compact(self, ctx, start, keep, count):
+        status = dev(np.full(len(start), -7, np.int32))
+        ctx.kv_compact(self.c, *(dev(np.asarray(x, np.int32)) for x in (start, keep, count)), status)
+        want = self.model.compact(start, np.asarray(keep), count)
+        assert status.cpu().numpy().tolist() == want.tolist()
+
+    def check(self, status=None):
+        torch.cuda.synchronize()
+        if status is not None:
+            assert int(self.status) == status
+        m = self.model
+        for name in ("table", "held", "lens", "refs"):
+            np.testing.assert_array_equal(getattr(self, name).cpu().numpy(), getattr(m, name), name)
+        for got, want in zip(self.pools, (m.k, m.v)):
+            got = got.view(torch.uint8).contiguous().cpu().numpy()
+            if self.layout == "HND":
+                got = got.transpose(0, 1, 3, 2, 4)
+            np.testing.assert_array_equal(got, want)
+        if self.layout == "mixed":  # the gaps
+            assert int(self.whole[..., -16:].max()) == 0
+        np.testing.assert_array_equal(m.refs, np.bincount(m.table[m.table >= 0],
+                                                          minlength=m.refs.size))
+
+
+LAYOUTS = ["NHD", "HND", "mixed"]
+
+
+# ---------------------------------------------------------------------------
+# Copy
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f16", 8), ("f32", 20), ("byte", 48)])
+@pytest.mark.parametrize("P,heads", [(1, 1), (16, 3), (5, 8), (64, 1)])
+def test_copy_pages(ctx, layout, dtype, dim, P, heads):
+    x = Cache(layers=3, pages=40, P=P, heads=heads, dim=dim, layout=layout, dtype=dtype, seed=P)
+    g = np.random.default_rng(P * 7 + heads)
+    order = g.permutation(40).astype(np.int32)
+    src, dst = order[:20], order[20:]
+    src[3], dst[5], src[6], dst[7] = -1, -1, 40, 2**31 - 1  # skipped
+    ctx.kv_copy_pages(x.c, dev(src), dev(dst))
+    x.model.copy_pages(src, dst)
+    x.check()
+    tokens = g.integers(-1, P + 2, 20).astype(np.int32)  # nothing, a part, all, clamped
+    ctx.kv_copy_pages(x.c, dev(dst), dev(src), 19, tokens=dev(tokens))
+    x.model.copy_pages(dst[:19], src[:19], tokens)
+    x.check()
+
+
+def test_copy_many_layers_and_one_entry(ctx):
+    x = Cache(layers=70, pages=3, P=16, heads=2, dim=64)
+    ctx.kv_copy_pages(x.c, dev(np.array([2], np.int32)), dev(np.array([0], np.int32)))
+    x.model.copy_pages([2], [0])
+    x.check()
+    ctx.kv_copy_pages(x.c, dev(np.zeros(0, np.int32)), dev(np.zeros(0, np.int32)))
+    x.check()
+
+
+def test_copy_past_32_bit_offsets(ctx):
+    # 5 GiB of one-layer pages; the last page lies past 2^32 bytes
+    pages, bytes_ = 80, 64 << 20
+    pool = torch.zeros(2, 1, pages, 64, 8, bytes_ // 512, dtype=torch.uint8, device="cuda")
+    pool[:, 0, 1] = 3
+    pool[0, 0, 1, 5] = 9
+    c = tb.kv_cache(pool[0], pool[1])
+    ctx.kv_copy_pages(c, dev(np.array([1], np.int32)), dev(np.array([pages - 1], np.int32)))
+    torch.cuda.synchronize()
+    assert torch.equal(pool[:, 0, 1], pool[:, 0, pages - 1])
+    assert int(pool[:, 0, 2:pages - 1].max()) == 0
+
+
+# ---------------------------------------------------------------------------
+# Resize
+# ---------------------------------------------------------------------------
+def test_resize_takes_the_lowest_free_pages_and_gives_back(ctx):
+    x = Cache(slots=4, width=6, pages=16, P=4)
+    assert x.resize(ctx, [5, 0, 9, 4]) == 0  # 2, 0, 3, 1 pages
+    x.check(0)
+    assert x.table[2, :4].tolist() == [2, 3, 4, -1]
+    x.set_lens([5, 0, 8, 1])
+    assert x.resize(ctx, [-1, 8, 4, 0]) == 0  # slot 2 gives two back, slot 3 its only one
+    x.check(0)
+    assert x.table[1, :2].tolist() == [6, 7]  # not yet the pages given back by the same call
+    assert x.resize(ctx, [24, 8, 4, 12]) == 0
+    x.check(0)
+
+
+def test_resize_refuses_as_a_whole(ctx):
+    x = Cache(slots=3, width=4, pages=7, P=4)
+    assert x.resize(ctx, [16, 4, 0]) == 0
+    x.check(0)
+    assert x.resize(ctx, [0, 16, 4]) == 2  # 4 more pages, 2 free: 2 missing; nothing given back
+    x.check(2)
+    assert x.resize(ctx, [-1, 17, 0]) == -1  # 5 pages in a row of 4
+    x.check(-1)
+    assert x.resize(ctx, [2**31 - 1, -1, -1]) == -1
+    x.check(-1)
+
+
+def test_resize_does_not_cut_inside_a_shared_page(ctx):
+    x = Cache(slots=3, width=4, pages=12, P=4)
+    x.resize(ctx, [9, 0, 0])
+    x.set_lens([9, 0, 0])
+    assert x.fork(ctx, [0, 0, -1]) == 0
+    x.check(0)
+    assert x.resize(ctx, [6, -1, -1]) == -1  # page 1 is shared and would be written again
+    x.check(-1)
+    assert x.resize(ctx, [4, -1, -1]) == 0
+    x.check(0)
+
+
+@pytest.mark.parametrize("slots,width,pages,P", [(1, 1, 1, 1), (70, 40, 2500, 8), (1500, 3, 6000, 16),
+                                                 (8192, 2, 20000, 1), (3, 3000, 70001, 5)])
+def test_resize_random(ctx, slots, width, pages, P):
+    x = Cache(layers=1, heads=1, dim=8, slots=slots, width=width, pages=pages, P=P)
+    g = np.random.default_rng(slots + pages)
+    for _ in range(4):
+        capacity = g.integers(-1, width * P + 1, slots)
+        capacity[g.random(slots) < 0.3] = 0
+        want = x.resize(ctx, capacity.tolist())
+        x.check(want)
+        x.set_lens(np.minimum(x.model.held * P, g.integers(0, width * P + 1, slots)))
+
+
+# ---------------------------------------------------------------------------
+# Fork
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("P,lens", [(4, [9, 8, 1, 0, 4]), (1, [3, 1, 0, 6, 2]), (5, [5, 29, 30, 4, 6])])
+def test_fork(ctx, layout, P, lens):
+    x = Cache(slots=5, width=6, pages=60, P=P, layout=layout)
+    x.resize(ctx, [min(n + 6, 6 * P) for n in lens])  # spare pages beyond the tokens
+    x.set_lens(lens)
+    for parents in ([0, 0, 0, 3, 4], [1, 0, 1, -1, 2], [4, 4, 4, 4, 4], [0, 1, 2, 3, 4], [-1, -1, 3, 3, -5],
+                    [-1] * 5):
+        assert x.fork(ctx, parents) == 0
+        x.check(0)
+    assert int(x.refs.max()) == 0
+
+
+def test_fork_refuses_as_a_whole(ctx):
+    x = Cache(slots=4, width=3, pages=5, P=4)
+    x.resize(ctx, [6, 5, 0, 0])
+    x.set_lens([6, 5, 0, 0])
+    assert x.fork(ctx, [0, 1, 0, 1]) == 1  # one page free, two part-filled pages to copy
+    x.check(1)
+    assert x.fork(ctx, [0, 1, 4, -1]) == -1
+    x.check(-1)
+    assert x.fork(ctx, [-1, 1, 1, -1]) == 0
+    x.check(0)
+
+
+@pytest.mark.parametrize("slots,width,P,pages", [(300, 20, 3, 8000), (8192, 1, 2, 20000), (12, 700, 16, 9000)])
+def test_fork_random(ctx, slots, width, P, pages):
+    x = Cache(layers=2, heads=1, dim=8, slots=slots, width=width, pages=pages, P=P)
+    g = np.random.default_rng(slots)
+    x.resize(ctx, np.full(slots, width * P).tolist())
+    x.set_lens(g.integers(0, width * P + 1, slots))
+    for _ in range(3):
+        parents = g.integers(-1, slots, slots).tolist()
+        x.check(x.fork(ctx, parents))
+
+
+# ---------------------------------------------------------------------------
+# Compact
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("P,dtype,dim", [(4, "bf16", 64), (1, "f32", 4), (16, "byte", 16)])
+def test_compact(ctx, layout, P, dtype, dim):
+    width = 64 // P
+    x = Cache(slots=5, width=width, pages=5 * width, P=P, layout=layout, dtype=dtype, dim=dim, heads=3)
+    x.resize(ctx, [64] * 5)
+    x.set_lens([64] * 5)
+    g = np.random.default_rng(P)
+    keep = np.sort([g.permutation(40)[:30] for _ in range(5)], axis=1)
+    keep[3] = np.arange(30)  # nothing moves
+    keep[4] = np.arange(30) + 10  # each token onto the place that the token ten before it left
+    x.compact(ctx, [20, 0, 33 - 9, 5, 0], keep, [30, 17, 0, 30, 30])
+    x.check()
+    x.compact(ctx, [1, 2, 3, 4, 5], keep[:, :1], [1, -1, 0, 1, 1])
+    x.check()
+
+
+def test_compact_long_list(ctx):
+    x = Cache(layers=1, slots=2, width=150, pages=300, P=8, heads=1, dim=8)
+    x.resize(ctx, [1200, 1200])
+    x.set_lens([1200, 1100])
+    g = np.random.default_rng(3)
+    keep = np.stack([np.sort(g.permutation(1150)[:1001]), np.concatenate([np.arange(500), np.arange(501) + 600])])
+    x.compact(ctx, [50, 0], keep, [1001, 1001])
+    x.check()
+
+
+def test_compact_refusals(ctx):
+    x = Cache(slots=6, width=4, pages=40, P=4)
+    x.resize(ctx, [16] * 5 + [0])
+    x.set_lens([9, 16, 16, 16, 16, 0])
+    assert x.fork(ctx, [0, 1, 2, 3, 4, 0]) == 0
+    # slot 0 shares its first two pages: a move inside them, a cut inside them, a move after them
+    for start, keep, count in ((0, [0, 2], 2), (5, [0, 1], 0), (8, [0, 1], 1)):
+        x.compact(ctx, [start, 0, 0, 0, 0, 0], [keep, [1, 0], [0, 16], [0, 0], [-1, 2], [0, 1]],
+                  [count, 2, 2, 2, 2, 1])
+        x.check()
+    x.compact(ctx, [0, 15, -1, 13, 0, 0], [[0, 1]] * 6, [3, 2, 1, 2, -1, 0])
+    x.check()
+
+
+# ---------------------------------------------------------------------------
+# Together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("seed", range(6))
+def test_random_steps(ctx, seed):
+    """Resizes, forks and compactions in a random order."""
+    g = np.random.default_rng(100 + seed)
+    slots, P = int(g.integers(2, 12)), int(g.choice([1, 3, 4, 16]))
+    width = int(g.integers(2, 20))
+    x = Cache(slots=slots, width=width, pages=slots * width, P=P, layout=LAYOUTS[seed % 3], seed=seed)
+    for _ in range(25):
+        what = g.integers(0, 4)
+        if what == 0:
+            x.check(x.resize(ctx, g.integers(-1, width * P + 1, slots).tolist()))
+        elif what == 1:  # tokens appended inside the pages held
+            x.set_lens([int(g.integers(n, h * P + 1)) for n, h in zip(x.model.lens, x.model.held)])
+        elif what == 2:
+            x.check(x.fork(ctx, g.integers(-1, slots, slots).tolist()))
+        else:
+            start = [int(g.integers(0, n + 1)) for n in x.model.lens]
+            most = max(int(n) - s for n, s in zip(x.model.lens, start))
+            keep = np.sort(np.stack([g.permutation(most + 1) for _ in range(slots)])[:, :most // 2 + 1], axis=1)
+            count = g.integers(-1, keep.shape[1] + 1, slots).tolist()
+            x.compact(ctx, start, keep, count)
+            x.check()
+
+
+def test_side_stream_and_graph(ctx):
+    """Calls on a stream of their own, and replayed from a graph."""
+    x = Cache(slots=3, width=4, pages=20, P=4)
+    stream = torch.cuda.Stream()
+    capacity, status = dev(np.array([5, 9, 0], np.int32)), x.status
+    out = [torch.empty_like(t) for t in (x.table, x.held, x.lens)]
+    parents = dev(np.array([0, 1, 1], np.int32))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        ctx.kv_resize(x.c, capacity, status, stream)
+        ctx.kv_fork(x.c, parents, *out, status, stream)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert x.model.resize([5, 9, 0]) == 0 and x.model.fork([0, 1, 1]) == 0
+    x.table, x.held, x.lens = out
+    x.check(0)
+
+
+# ---------------------------------------------------------------------------
+# Refusals
+# ---------------------------------------------------------------------------
+def refused(code, call, *args, **kw):
+    with pytest.raises(tb.TBError) as e:
+        call(*args, **kw)
+    assert e.value.code == code
+
+
+def test_refusals(ctx):
+    x = Cache()
+    one, many = x.status, dev(np.zeros(5, np.int32))
+    s = x.c.struct
+
+    def with_(**kw):
+        old = {n: getattr(s, n) for n in kw}
+        for n, v in kw.items():
+            setattr(s, n, v)
+        return lambda: [setattr(s, n, v) for n, v in old.items()]
+
+    for bad in (dict(k=None), dict(layers=0), dict(page_tokens=0), dict(dtype=9), dict(k=s.k + 8),
+                dict(page_stride=s.page_stride + 8), dict(token_stride=16), dict(head_stride=0),
+                dict(pages=2**31 - 1, page_stride=2**60)):
+        undo = with_(**bad)
+        refused(tb.TB_EINVAL, ctx.kv_copy_pages, x.c, many, many)
+        undo()
+    undo = with_(layers=70000)
+    refused(tb.TB_ENOTSUP, ctx.kv_copy_pages, x.c, many, many)
+    undo()
+    refused(tb.TB_EINVAL, ctx.kv_copy_pages, x.c, many, many, -1)
+    for bad in (dict(table=None), dict(refs=None), dict(held=None), dict(lens=None), dict(table_width=0)):
+        undo = with_(**bad)
+        refused(tb.TB_EINVAL, lambda: ctx._ok(tb.lib.tb_kv_resize(
+            ctx.handle, x.c.ref, many.data_ptr(), one.data_ptr(), None), ""))
+        undo()
+    undo = with_(table_width=2**30)
+    refused(tb.TB_ENOTSUP, lambda: ctx._ok(tb.lib.tb_kv_resize(
+        ctx.handle, x.c.ref, many.data_ptr(), one.data_ptr(), None), ""))
+    undo()
+    undo = with_(slots=tb.TB_KV_MAX_SLOTS + 1)
+    refused(tb.TB_ENOTSUP, lambda: ctx._ok(tb.lib.tb_kv_resize(
+        ctx.handle, x.c.ref, many.data_ptr(), one.data_ptr(), None), ""))
+    undo()
+    refused(tb.TB_EINVAL, ctx.kv_fork, x.c, many, x.table, torch.empty_like(x.held), torch.empty_like(x.lens), one)
+    refused(tb.TB_EINVAL, ctx.kv_fork, x.c, many, torch.empty_like(x.table), x.held, torch.empty_like(x.lens), one)
+    with pytest.raises(ValueError):
+        ctx.kv_resize(x.c, dev(np.zeros(4, np.int32)), one)
+    with pytest.raises(TypeError):
+        ctx.kv_resize(x.c, dev(np.zeros(5, np.int64)), one)
+    with pytest.raises(ValueError):
+        ctx.kv_copy_pages(x.c, many, many, 6)
+    with pytest.raises(TypeError):
+        ctx.kv_copy_pages(x.c, many.cpu(), many)
+    with pytest.raises(ValueError):
+        tb.kv_cache(x.pools[0], x.pools[1][:, :1])
+    with pytest.raises(ValueError):
+        tb.kv_cache(x.pools[0], None)
+    x.check()
