@@ -78,6 +78,9 @@ struct tb_ctx {
     // Host-mapped word the bulk reduce kernel sets if a bounded wait expired.
     volatile uint32_t *reduce_status = nullptr;
     uint32_t *reduce_status_dev = nullptr;
+    // The same for the tree attention.
+    volatile uint32_t *tree_status = nullptr;
+    uint32_t *tree_status_dev = nullptr;
 
     std::vector<cudaEvent_t> events;  // timing events of tb_run_transfer
     std::vector<float> iter_ms;
@@ -139,6 +142,12 @@ int ctx_num_sms(const tb_ctx *ctx)
 const tb_options &ctx_options(const tb_ctx *ctx)
 {
     return ctx->opt;
+}
+
+volatile uint32_t *ctx_tree_status(const tb_ctx *ctx, uint32_t **dev)
+{
+    *dev = ctx->tree_status_dev;
+    return ctx->tree_status;
 }
 
 }  // namespace tb
@@ -678,15 +687,18 @@ int tb_create(tb_ctx **out, int device, const tb_options *opt)
     ctx->gate_flag = static_cast<volatile uint32_t *>(gate);
     ctx->gate_status = ctx->gate_flag + 1;
     ctx->reduce_status = ctx->gate_flag + 2;
+    ctx->tree_status = ctx->gate_flag + 3;
     ctx->gate_flag[0] = 0;
     ctx->gate_status[0] = 0;
     ctx->reduce_status[0] = 0;
+    ctx->tree_status[0] = 0;
     void *dgate = nullptr;
     if (cudaHostGetDevicePointer(&dgate, gate, 0) != cudaSuccess)
         return bail(TB_ECUDA);
     ctx->gate_flag_dev = static_cast<uint32_t *>(dgate);
     ctx->gate_status_dev = ctx->gate_flag_dev + 1;
     ctx->reduce_status_dev = ctx->gate_flag_dev + 2;
+    ctx->tree_status_dev = ctx->gate_flag_dev + 3;
 
     for (int k = 0; k <= tb::kShortShapes; ++k) {
         const int per_sm = tb::batch_ctas_per_sm(k);

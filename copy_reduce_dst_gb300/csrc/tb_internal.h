@@ -19,6 +19,9 @@ int cuda_fail(tb_ctx *ctx, cudaError_t e, const char *what);
 int ctx_device(const tb_ctx *ctx);
 int ctx_num_sms(const tb_ctx *ctx);
 const tb_options &ctx_options(const tb_ctx *ctx);
+// Host-mapped word the tree attention sets if a bounded wait expired, and its
+// device address.
+volatile uint32_t *ctx_tree_status(const tb_ctx *ctx, uint32_t **dev);
 
 // Makes a device current for the scope and restores the caller's after.
 class DeviceScope {

@@ -95,8 +95,8 @@ int view_of(tb_ctx *ctx, const tb_kv_cache *cache, bool pools, bool table, const
             return fail(ctx, TB_EINVAL,
                         "%s: null table, held, lens or refs, or slots or table_width < 1", who);
         // Positions of a slot are counted in 32 bits.
-        if (c.table_width > INT_MAX / c.page_tokens)
-            return fail(ctx, TB_ENOTSUP, "%s: table_width * page_tokens exceeds 2^31 - 1", who);
+        if (c.table_width > (1 << 30) / c.page_tokens)
+            return fail(ctx, TB_ENOTSUP, "%s: table_width * page_tokens exceeds 2^30", who);
         v.table = c.table;
         v.held = c.held;
         v.lens = c.lens;
@@ -228,6 +228,12 @@ int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream)
     if (!t)
         return fail(ctx, TB_EINVAL, "tree_attention: null arguments");
     tb::TreePlan p{};
+    volatile uint32_t *expired = tb::ctx_tree_status(ctx, &p.status);
+    if (*expired != 0u) {
+        *expired = 0u;
+        return fail(ctx, TB_ETIMEOUT, "an earlier tree attention on this context stopped early: a "
+                                      "bounded wait inside the kernel expired");
+    }
     int rc = view_of(ctx, t->cache, true, true, "tree_attention", &p.c);
     if (rc != TB_OK)
         return rc;
@@ -242,8 +248,8 @@ int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream)
         return fail(ctx, TB_ENOTSUP, "tree_attention: head_dim %d is more than 128", c.head_dim);
     if (t->seqs > TB_TREE_MAX_SEQS)
         return fail(ctx, TB_ENOTSUP, "tree_attention: more than %d sequences", TB_TREE_MAX_SEQS);
-    if (t->rows > INT_MAX / t->q_heads)
-        return fail(ctx, TB_ENOTSUP, "tree_attention: rows * q_heads exceeds 2^31 - 1");
+    if (t->rows > (1 << 29) || t->rows > INT_MAX / t->q_heads)
+        return fail(ctx, TB_ENOTSUP, "tree_attention: rows exceeds 2^29 or rows * q_heads 2^31 - 1");
     if (!t->seq_slots && t->seqs > c.slots)
         return fail(ctx, TB_EINVAL, "tree_attention: more sequences than slots");
     if (!isfinite(t->scale))
@@ -281,6 +287,7 @@ int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream)
     p.mask = t->mask;
     p.workspace = t->workspace;
     p.scale = t->scale;
+    p.wait_ns = tb::ctx_options(ctx).kernel_wait_ns;
     tb::DeviceScope scope(tb::ctx_device(ctx));
     return launched(ctx,
                     tb::launch_tree(p, tb::ctx_num_sms(ctx), tb::ctx_options(ctx).use_pdl != 0,

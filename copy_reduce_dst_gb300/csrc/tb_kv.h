@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "tb.h"
+#include "tb_internal.h"
 
 namespace tb {
 
@@ -44,6 +45,8 @@ struct TreePlan {
     const uint32_t *mask;
     void *workspace;
     float scale;
+    uint32_t *status;  // device-visible: 1 if a bounded wait expired
+    uint64_t wait_ns;  // limit of each wait inside the kernel
 };
 
 uint64_t tree_workspace_bytes(int num_sms, int head_dim);

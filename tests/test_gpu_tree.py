@@ -334,3 +334,14 @@ def test_refusals(ctx):
     # nothing to do is no error
     ctx.tree_attention(cache, 0, q[:0], q_start[:1], mask[:0], out[:0], work)
     torch.cuda.synchronize()
+
+
+def test_expired_wait_is_reported_by_the_next_call(ctx):
+    """A limit of 0 lets the kernel's first wait run out: it stops, and the next call says so."""
+    with tb.Context(0, tb.options(kernel_wait_ns=0)) as hasty:
+        c = Case(hasty, [3000], [4], seed=16)
+        c.run()
+        with pytest.raises(tb.TBError) as e:
+            hasty.tree_attention(*c.args, **c.kw)
+        assert e.value.code == tb.TB_ETIMEOUT
+    Case(ctx, [3000], [4], seed=16).check()
