@@ -2,6 +2,7 @@
 // softmax(scale q K^T + mask) V in one pass over the positions, matrix products
 // on tcgen05 with scores, weights and output sums in tensor memory.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,7 +29,8 @@ constexpr int kTile = 128;       // positions of a tile
 constexpr int kRowTile = 128;    // rows of one matrix instruction
 constexpr int kUnitRows = 256;   // rows of a unit: two row tiles
 constexpr int kThreads = 384;    // warps 0-7: softmax; 8-10: loads; 11: matrix products
-constexpr int kLoadWarps = 3;
+constexpr int kLoadWarps = 3;    // ... all of them where threads load
+constexpr int kFixWarps = 2;     // ... else one asks for tiles, two look drafts over
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;    // rows of a unit one CTA of k_tree_join takes
 
@@ -189,7 +191,7 @@ struct Layout {
     static constexpr int kStages = DP == 128 ? 5 : 8;
     static constexpr uint32_t kQ = 0, kRing = 2 * kOperand, kEnd = kRing + kStages * kOperand;
     static constexpr uint32_t kBars = kEnd;              // barriers
-    static constexpr uint32_t kMisc = kBars + 256;
+    static constexpr uint32_t kMisc = kBars + 320;
     static constexpr uint32_t kBytes = kMisc + 1536;
 };
 
@@ -204,6 +206,7 @@ enum {
     kGive = 23,       // stream 1's half of the sums is in shared memory
     kTaken = 24,      // ... and has been read
     kLast = 25,       // after an expired wait: the products asked for are done
+    kTail = 32,       // [stage] values to be looked over have landed
 };
 
 struct Misc {
@@ -298,12 +301,148 @@ __device__ __forceinline__ bool clean(uint32_t &pair)
 }
 
 // ---------------------------------------------------------------------------
-// Loads: each warp takes 16 rows of a tile at a time, its lanes 16 bytes each,
-// by asynchronous copies; what has no position reads as zeros.  A value that a
-// row does not see must not reach it, not even times a weight of 0: drafted
-// values that are not finite are zeroed here and added at the end to the rows
-// that see them.
+// Loads.  A value that a row does not see must not reach it, not even times a
+// weight of 0: values past the sequence's end read as zeros, and drafted values
+// that are not finite are zeroed in shared memory and added at the unit's end
+// to the rows that see them.
 // ---------------------------------------------------------------------------
+
+// Which tile (*i of the unit's n) of which pool is the unit's item-th load.
+__device__ __forceinline__ bool is_value(bool two, int item, int n, int *i)
+{
+    if (two) {
+        *i = item >> 1;
+        return item & 1;
+    }
+    const int ahead = min(n, 2), rest = item - ahead, pairs = max(n - 2, 0);
+    if (rest < 0) {
+        *i = item;
+        return false;
+    }
+    if (rest >= 2 * pairs) {  // V0 K2 V1 K3 ... and then the last values
+        *i = rest - pairs;
+        return true;
+    }
+    *i = rest & 1 ? (rest >> 1) + 2 : rest >> 1;
+    return !(rest & 1);
+}
+
+// Pages of a multiple of 8 tokens: one lane per box of `box` positions (the
+// largest power of two that divides a page, at most a tile), by tensor maps of
+// (dim, token, head, page); positions without a page read as zeros.
+struct Maps {
+    CUtensorMap pool[2];
+    int box;
+    int token_dim, head_dim;  // places of the token and the head among dims 1..3
+};
+
+template <int DP>
+__device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Walk walk)
+{
+    using L = Layout<DP>;
+    const KvView &c = p.c;
+    const int lane = threadIdx.x & 31, boxes = kTile / maps.box;
+    uint32_t k = 0, tail_use = 0, tail_parity = 0;  // by stage: its last load, uses of kTail
+    Unit u;
+    while (walk.next(u)) {
+        const int n = u.tiles();
+        for (int item = 0; item < 2 * n; ++item, ++k) {
+            int i;
+            const bool value = is_value(u.two(), item, n, &i);
+            const int j = u.j0 + i, pos = j * kTile + lane * maps.box;
+            int page = c.pages;  // past the pool: zeros
+            if (lane < boxes && pos < u.s.end && pos / c.page_tokens < c.width) {
+                page = __ldg(c.table + (int64_t)u.s.slot * c.width + pos / c.page_tokens);
+                if (page < 0 || page > c.pages)
+                    page = c.pages;
+            }
+            const uint32_t stage = k % L::kStages, tile = cta.smem + L::kRing + stage * L::kOperand;
+            const bool tail = value && u.tail(j);
+            bool ok = true;
+            if (lane == 0) {
+                ok = cta.wait(kEmpty + stage, (k / L::kStages & 1) ^ 1);
+                if (ok) {
+                    mbar_expect_tx(cta.bar((tail ? kTail : kFull) + stage), L::kOperand);
+                    if (!tail)
+                        mbar_arrive(cta.bar(kFull + stage));
+                }
+            }
+            if (!__all_sync(0xffffffffu, ok)) {
+                // Let the tiles asked for land (bounded).
+                for (uint32_t x = k - min(k, (uint32_t)L::kStages); x < k; ++x) {
+                    const uint32_t s = x % L::kStages;
+                    if (tail_use >> s & 1)
+                        mbar_wait_bounded(cta.bar(kTail + s), tail_parity >> s & 1 ^ 1);
+                    else
+                        mbar_wait_bounded(cta.bar(kFull + s), x / L::kStages & 1);
+                }
+                return;
+            }
+            tail_use = (tail_use & ~(1u << stage)) | (uint32_t)tail << stage;
+            tail_parity ^= (uint32_t)tail << stage;
+            if (lane < boxes) {
+                const int token = pos % c.page_tokens;
+                int at[4] = {0, page, page, page};
+                at[maps.token_dim] = token;
+                at[maps.head_dim] = u.head;
+#pragma unroll
+                for (int h = 0; h < DP / 64; ++h)
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::"
+                        "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                            tile + h * (128 * 128) + lane * maps.box * 128),
+                        "l"(&maps.pool[value]), "r"(64 * h), "r"(at[1]), "r"(at[2]), "r"(at[3]),
+                        "r"(cta.bar((tail ? kTail : kFull) + stage))
+                        : "memory");
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Looks over the values of the tiles that hold drafts.
+template <int DP, bool BF16>
+__device__ void fix_role(const TreePlan &p, const Cta &cta, Walk walk)
+{
+    using L = Layout<DP>;
+    constexpr int kChunks = DP / 8;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x - 9 * 32;
+    uint32_t k = 0, parity = 0;
+    Unit u;
+    for (int units = 0; walk.next(u); ++units) {
+        const int n = u.tiles();
+        for (int i = max(u.s.n / kTile - u.j0, 0); i < n; ++i) {
+            const uint32_t item = k + value_item(u.two(), i, n), stage = item % L::kStages;
+            const uint32_t tile = cta.smem + L::kRing + stage * L::kOperand;
+            if (!__all_sync(0xffffffffu, cta.wait(kTail + stage, parity >> stage & 1)))
+                return;
+            parity ^= 1u << stage;
+            const int base = (u.j0 + i) * kTile;
+            for (int x = max(u.s.n - base, 0) * kChunks + tid; x < kTile * kChunks; x += 32 * kFixWarps) {
+                const uint32_t at = tile + swizzled(x / kChunks, x % kChunks);
+                if (base + x / kChunks >= u.s.end) {
+                    sts16(at, uint4{0, 0, 0, 0});
+                } else {
+                    uint4 v = lds16(at);
+                    const bool a = clean<BF16>(v.x), b = clean<BF16>(v.y), d = clean<BF16>(v.z),
+                               e = clean<BF16>(v.w);
+                    if (a || b || d || e) {
+                        sts16(at, v);
+                        cta.misc->bad[units & 7] = units + 1;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(cta.bar(kFull + stage));
+        }
+        k += 2 * n;
+    }
+}
+
+// Any other page: each of three warps takes 16 rows of a tile at a time, its
+// lanes 16 bytes each, by asynchronous copies, and looks over its own drafts.
 constexpr int kInFlight = 2;  // tiles behind the one being requested
 
 template <int DP, bool BF16>
@@ -354,20 +493,8 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
     for (; walk.next(u); ++units) {
         const int n = u.tiles(), items = 2 * n;
         for (int item = 0; item < items; ++item, ++k) {
-            // Which tile of which pool comes now.
-            bool value;
             int i;
-            if (u.two()) {
-                value = item & 1;
-                i = item >> 1;
-            } else if (item < min(n, 2)) {
-                value = false;
-                i = item;
-            } else {
-                const int rest = item - min(n, 2);  // V0 K2 V1 K3 ... then the last values
-                value = rest >= 2 * max(n - 2, 0) || !(rest & 1);
-                i = rest >= 2 * max(n - 2, 0) ? rest - max(n - 2, 0) : value ? rest >> 1 : (rest >> 1) + 2;
-            }
+            const bool value = is_value(u.two(), item, n, &i);
             const int base = (u.j0 + i) * kTile;
             const uint32_t stage = k % L::kStages, tile = cta.smem + L::kRing + stage * L::kOperand;
             bool ok = lane != 0 || cta.wait(kEmpty + stage, (k / L::kStages & 1) ^ 1);
@@ -808,8 +935,9 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
     }
 }
 
-template <int DP, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1) k_tree(const TreePlan p)
+template <int DP, bool BF16, bool BOXES>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_tree(const __grid_constant__ TreePlan p, const __grid_constant__ Maps maps)
 {
     using L = Layout<DP>;
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -823,7 +951,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree(const TreePlan p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kStages; ++i) {
-            mbar_init_count(cta.bar(kFull + i), kLoadWarps);
+            mbar_init_count(cta.bar(kFull + i), BOXES ? kFixWarps : kLoadWarps);
+            mbar_init_count(cta.bar(kTail + i), 1);
             mbar_init_count(cta.bar(kEmpty + i), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -857,10 +986,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree(const TreePlan p)
             softmax_role<DP, BF16>(p, cta, walk, blockIdx.x);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            if (warp < 8 + kLoadWarps)
+            if (warp == 8 + kLoadWarps) {
+                if (lane == 0)
+                    product_role<DP, BF16>(p, cta, walk);
+            } else if (!BOXES) {
                 load_role<DP, BF16>(p, cta, walk);
-            else if (lane == 0)
-                product_role<DP, BF16>(p, cta, walk);
+            } else if (warp == 8) {
+                box_role<DP>(p, maps, cta, walk);
+            } else {
+                fix_role<DP, BF16>(p, cta, walk);
+            }
         }
     }
     // After an expired wait products may still run: let them end (bounded).
@@ -954,13 +1089,81 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Tensor maps of the two pools; false where the pages' shape does not allow
+// them (the kernel then loads by threads).
+bool make_maps(const TreePlan &p, Maps *m)
+{
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    const KvView &c = p.c;
+    if (!encode || c.page_tokens % 8)
+        return false;
+    m->box = 8;
+    while (m->box < kTile && c.page_tokens % (2 * m->box) == 0)
+        m->box *= 2;
+    // Dimensions in the order of their strides.
+    struct Dim {
+        int64_t stride;
+        uint32_t extent, box;
+        int what;  // 0 token, 1 head, 2 page
+    } dim[3] = {{c.token_stride, (uint32_t)c.page_tokens, (uint32_t)m->box, 0},
+                {c.head_stride, (uint32_t)c.heads, 1, 1},
+                {c.page_stride, (uint32_t)c.pages, 1, 2}};
+    for (Dim &d : dim)
+        if (d.extent == 1)  // its stride says nothing
+            d.stride = c.row_bytes;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (dim[j].stride > dim[j + 1].stride) {
+                const Dim d = dim[j];
+                dim[j] = dim[j + 1];
+                dim[j + 1] = d;
+            }
+    cuuint64_t extent[4] = {(cuuint64_t)p.head_dim}, stride[3];
+    cuuint32_t box[4] = {64}, step[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        extent[i + 1] = dim[i].extent;
+        stride[i] = (cuuint64_t)dim[i].stride;
+        box[i + 1] = dim[i].box;
+        if (dim[i].what == 0)
+            m->token_dim = i + 1;
+        if (dim[i].what == 1)
+            m->head_dim = i + 1;
+    }
+    for (int x = 0; x < 2; ++x)
+        if (encode(&m->pool[x],
+                   p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   c.pool[x], extent, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
+template <int DP, bool BF16, bool BOXES>
+cudaError_t launch_loads(const TreePlan &p, const Maps &maps, int num_sms, bool pdl, cudaStream_t stream)
+{
+    constexpr size_t smem = Layout<DP>::kBytes + 1024;
+    if (resident_ctas((const void *)k_tree<DP, BF16, BOXES>, kThreads, smem) < 1)
+        return cudaErrorInvalidConfiguration;
+    return launch(k_tree<DP, BF16, BOXES>, dim3(num_sms), kThreads, smem, pdl, stream, p, maps);
+}
+
 template <int DP, bool BF16>
 cudaError_t launch_dim(const TreePlan &p, int num_sms, bool pdl, cudaStream_t stream)
 {
-    constexpr size_t smem = Layout<DP>::kBytes + 1024;
-    if (resident_ctas((const void *)k_tree<DP, BF16>, kThreads, smem) < 1)
-        return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch(k_tree<DP, BF16>, dim3(num_sms), kThreads, smem, pdl, stream, p);
+    alignas(64) Maps maps;
+    const cudaError_t e = make_maps(p, &maps)
+                              ? launch_loads<DP, BF16, true>(p, maps, num_sms, pdl, stream)
+                              : launch_loads<DP, BF16, false>(p, maps, num_sms, pdl, stream);
     if (e != cudaSuccess || num_sms < 2)
         return e;
     return launch(k_tree_join<DP, BF16>, dim3(num_sms - 1, kUnitRows / kJoinRows), kJoinThreads, 0, pdl,
