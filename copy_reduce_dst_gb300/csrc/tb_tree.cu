@@ -36,7 +36,7 @@ constexpr int kRowTile = 128;    // rows of one matrix instruction
 constexpr int kLoadWarps = 3;    // load by threads, or ...
 constexpr int kFixWarps = 2;     // ... one asks for tiles and two look drafts over
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 32;    // rows of a unit one CTA of k_tree_join takes
+constexpr int kJoinRows = 16;    // rows of a unit one CTA of k_tree_join takes
 
 struct Seq {
     int slot, row0, T, n, end, tiles, units;  // units per cache head
@@ -63,9 +63,9 @@ __device__ __forceinline__ int64_t seq_work(const TreePlan &p, int b, int unit_r
 }
 
 // a / b for 0 <= a, 0 < b; 64-bit divisions cost hundreds of cycles.
-__device__ __forceinline__ int64_t divide(int64_t a, int b)
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
 {
-    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 struct Place {
@@ -605,25 +605,141 @@ __device__ __forceinline__ float *part_of(const TreePlan &p, int slot)
     return static_cast<float *>(p.workspace) + slot * part_floats(S::kUnitRows, S::DP);
 }
 
-// The bits of mask row `row` from draft `d` (possibly negative) on, for 32
-// positions: committed ones are seen, drafts from T on are not.
-__device__ __forceinline__ uint32_t seen_word(const TreePlan &p, const Seq &s, int64_t row, int d)
+// Where run c begins inside a unit and no earlier run does: what is to be
+// joined.  Entry c of an array after the parts; rows = 0: nothing.
+struct Cut {
+    int row0, head, r0, rows, parts, unused[3];
+};
+
+template <class S>
+__device__ __forceinline__ Cut *cuts_of(const TreePlan &p, int ctas)
 {
-    if (d <= -32)
-        return 0xffffffffu;
-    const uint32_t *words = p.mask + row * p.mask_words;
-    auto word = [&](int w) { return w < p.mask_words ? __ldg(words + w) : 0u; };
-    uint32_t v;
-    if (d < 0) {
-        v = word(0);
-        if (s.T < 32)
-            v &= (1u << s.T) - 1;
-        return v << -d | (0xffffffffu >> (32 + d));
+    return reinterpret_cast<Cut *>(part_of<S>(p, 2 * ctas));
+}
+
+template <class S>
+__device__ void note_cut(const TreePlan &p, const Place &place, Walk walk)
+{
+    Cut cut{};
+    Unit u;
+    if ((int)blockIdx.x < place.ctas && walk.next(u) && u.j0 > 0) {
+        const int64_t begin = place.at - u.j0, end = begin + u.s.tiles;
+        if (place.start(blockIdx.x - 1) <= begin) {
+            int last = (int)min(divide(end * place.ctas, place.total), (int64_t)place.ctas - 1);
+            while (place.start(last) >= end)
+                --last;
+            while (last + 1 < place.ctas && place.start(last + 1) < end)
+                ++last;
+            cut = Cut{u.s.row0, u.head, u.r0, u.rows, last - (int)blockIdx.x + 2, {}};
+        }
     }
-    if (d >= s.T)
-        return 0;
-    v = __funnelshift_r(word(d >> 5), word((d >> 5) + 1), d & 31);
-    return s.T - d < 32 ? v & ((1u << (s.T - d)) - 1) : v;
+    cuts_of<S>(p, gridDim.x)[blockIdx.x] = cut;
+}
+
+// A row of the mask.  The first 64 drafts' bits are read when the unit begins;
+// by the time they are needed they are there.
+struct MaskRow {
+    const uint32_t *words;
+    int count, T;
+    uint32_t first, second;
+    __device__ MaskRow(const TreePlan &p, const Seq &s, int64_t row)
+        : words(p.mask + row * p.mask_words), count(p.mask_words), T(s.end > 0 ? s.T : 0)
+    {
+        first = count > 0 ? __ldg(words) : 0;
+        second = count > 1 ? __ldg(words + 1) : 0;
+    }
+    __device__ uint32_t word(int w) const
+    {
+        return w == 0 ? first : w == 1 ? second : w < count ? __ldg(words + w) : 0;
+    }
+    // Bits for 32 positions from draft d (negative: committed positions, seen)
+    // on; drafts from T on are not seen.
+    __device__ uint32_t seen(int d) const
+    {
+        if (d <= -32)
+            return 0xffffffffu;
+        if (d >= T)
+            return 0;
+        const int w = d >> 5;  // -1 for the word before the first: all seen
+        uint32_t v = __funnelshift_r(w < 0 ? 0xffffffffu : word(w), word(w + 1), d & 31);
+        return T - d < 32 ? v & ((1u << (T - d)) - 1) : v;
+    }
+};
+
+// The sums of a row of the unit, from its columns of tensor memory to the output
+// or, if the unit goes on in another run, to the workspace.  Whole warps call it.
+template <class S>
+__device__ __forceinline__ void write_unit(const TreePlan &p, const Cta &cta, const Unit &u, int run,
+                                           int mine, uint32_t sum_cols, float top, float sum, float c)
+{
+    if (mine - (int)(threadIdx.x & 31) >= u.rows)
+        return;
+    const bool whole = u.whole(), real = mine < u.rows;
+    const bool bad = *(volatile int *)&cta.misc->bad[u.number & 7] == u.number + 1;
+    const int r = min(u.r0 + mine, u.s.T * p.group - 1), draft = r / p.group;
+    const int64_t q_row = u.s.row0 + draft;
+    const int q_head = u.head * p.group + r - draft * p.group;
+    char *out = p.out + q_row * p.o_row + (int64_t)q_head * p.o_head;
+    float *part = part_of<S>(p, 2 * run + (u.j0 == 0 ? 1 : 0));
+    const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (real) {
+        if (!whole) {
+            part[mine] = top == -INFINITY ? top : top * c;
+            part[S::kUnitRows + mine] = sum;
+        } else if (p.lse) {
+            p.lse[q_row * p.q_heads + q_head] =
+                top == -INFINITY && sum == 0.0f ? -INFINITY : top * fabsf(p.scale) + logf(sum);
+        }
+    }
+#pragma unroll 1
+    for (int g = 0; g < S::DP / 32; ++g) {
+        uint32_t o[32];
+        tmem_load32(o, sum_cols + 32 * g);
+        tmem_wait_load(o);
+        if (!real)
+            continue;
+        if (bad) {
+            // Drafted values that are not finite, for the rows that see them.
+            const MaskRow mask(p, u.s, q_row);
+            const int from = max(u.j0 * kTile - u.s.n, 0), to = min(u.j1 * kTile - u.s.n, u.s.T);
+            for (int d = from; d < to; ++d) {
+                const int pos = u.s.n + d;
+                if (!(mask.seen(d) & 1u) || pos / p.c.page_tokens >= p.c.width)
+                    continue;
+                const int page = p.c.table[(int64_t)u.s.slot * p.c.width + pos / p.c.page_tokens];
+                if (page < 0 || page >= p.c.pages)
+                    continue;
+                const char *v = p.c.pool[1] + page * p.c.page_stride +
+                                pos % p.c.page_tokens * p.c.token_stride + u.head * p.c.head_stride;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (32 * g + i < p.head_dim) {
+                        const uint32_t e = reinterpret_cast<const uint16_t *>(v)[32 * g + i];
+                        const uint32_t big = S::BF16 ? 0x7f80u : 0x7c00u, frac = S::BF16 ? 0x7fu : 0x3ffu;
+                        if ((e & big) == big)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) +
+                                                   (e & frac ? NAN : e >> 15 ? -INFINITY : INFINITY));
+                    }
+            }
+        }
+        if (whole) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (32 * g + 8 * w < p.head_dim) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = pack16<S::BF16>(__uint_as_float(o[8 * w + 2 * i]) * inv,
+                                               __uint_as_float(o[8 * w + 2 * i + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(out + (32 * g + 8 * w) * 2) = uint4{v[0], v[1], v[2], v[3]};
+                }
+        } else {
+            uint4 *to = reinterpret_cast<uint4 *>(part + 2 * S::kUnitRows + mine * S::DP + 32 * g);
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                to[w] = uint4{o[4 * w], o[4 * w + 1], o[4 * w + 2], o[4 * w + 3]};
+        }
+    }
 }
 
 template <class S>
@@ -635,93 +751,113 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
     const uint32_t lanes = cta.misc->tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t score_cols = lanes + S::score_col(stream), sum_cols = lanes + S::sum_col(stream);
     const uint32_t query = cta.smem + stream * S::kQuery;
-    const float scale = fabsf(p.scale), c = scale * 1.44269504088896340736f;
+    // A scale of 0 makes all weights equal: any c that leaves scores * c at 0
+    // does, and unlike 0 it leaves a hidden -inf alone.
+    const float scale = fabsf(p.scale), c = scale > 0.0f ? scale * 1.44269504088896340736f : 1e-38f;
     const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
     // The running maximum moves only when a row's grows by 8 powers of two:
     // weights stay below 2^8, exact in the 32-bit sums, and most tiles need no
     // pass over the output sums.
-    const float slack = c > 0.0f ? 8.0f / c : INFINITY;
+    const float slack = 8.0f / c;
     uint32_t tiles_seen = 0, sums_seen = 0;
 
-    auto advance = [&](Unit &u) {  // the next unit that has rows for this stream
-        while (walk.next(u))
-            if (u.rows > stream * kRowTile)
-                return true;
-        return false;
-    };
-    // Query rows of the stream's tile; rows past the unit's read as zeros.
-    uint4 q[kChunks];
-    auto fetch = [&](const Unit &u) {
+    Unit before, u;
+    bool begun = false;
+    float top = 0.0f, sum = 0.0f;
+    for (;;) {
+        bool more;  // a further unit has rows for this stream
+        while ((more = walk.next(u)) && u.rows <= stream * kRowTile)
+            ;
+        // The query rows of the stream's tile are on their way while the last
+        // unit's last product runs, and its first scores while the last sums
+        // are read: those are not written again before this stream's next
+        // weights.  Rows past the unit's read as zeros.
+        uint4 q[kChunks];
+        if (more) {
+            const int step = 128 / kChunks, d_step = step / p.group, h_step = step - d_step * p.group;
+            const int row = stream * kRowTile + tid / kChunks;
+            int draft = (u.r0 + row) / p.group, h = u.r0 + row - draft * p.group;
+            const char *from = p.q + (int64_t)u.head * p.group * p.q_head + tid % kChunks * 16;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int row = stream * kRowTile + i * (128 / kChunks) + tid / kChunks;
-            q[i] = uint4{0, 0, 0, 0};
-            if (row < u.rows && tid % kChunks * 16 < p.c.row_bytes) {
-                const int r = u.r0 + row, draft = r / p.group;
-                q[i] = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + (int64_t)(u.s.row0 + draft) * p.q_row +
-                    (int64_t)(u.head * p.group + r - draft * p.group) * p.q_head + tid % kChunks * 16));
+            for (int i = 0; i < kChunks; ++i) {
+                q[i] = uint4{0, 0, 0, 0};
+                if (row + i * step < u.rows && tid % kChunks * 16 < p.c.row_bytes)
+                    q[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        from + (int64_t)(u.s.row0 + draft) * p.q_row + (int64_t)h * p.q_head));
+                draft += d_step;
+                h += h_step;
+                if (h >= p.group) {
+                    h -= p.group;
+                    ++draft;
+                }
             }
         }
-    };
-    auto deliver = [&]() {
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            uint4 v = q[i];
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-            sts16(query + swizzled(kRowTile * 128, i * (128 / kChunks) + tid / kChunks, tid % kChunks), v);
+        if (begun) {
+            if (!__all_sync(0xffffffffu, cta.wait(kSums + stream, sums_seen++ & 1)))
+                return;
+            tc_fence_after();
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(cta.bar(kQuery + stream));
-    };
+        if (more) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                q[i].x ^= flip, q[i].y ^= flip, q[i].z ^= flip, q[i].w ^= flip;
+                sts16(query + swizzled(kRowTile * 128, i * (128 / kChunks) + tid / kChunks, tid % kChunks),
+                      q[i]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(cta.bar(kQuery + stream));
+        }
+        if (begun)
+            write_unit<S>(p, cta, before, run, stream * kRowTile + tid, sum_cols, top, sum, c);
+        if (!more)
+            return;
 
-    Unit u, after;
-    bool more = advance(u);
-    if (more) {
-        fetch(u);
-        deliver();
-    }
-    for (; more; u = after) {
         const int mine = stream * kRowTile + tid;         // row of the unit
         const bool active = mine - lane < u.rows;         // any row of the warp
-        const int r = min(u.r0 + mine, u.s.T * p.group - 1), draft = r / p.group;
-        const int64_t q_row = u.s.row0 + draft;
-        float top = -INFINITY, sum = 0.0f;
+        const MaskRow mask(p, u.s, u.s.row0 + min(u.r0 + mine, u.s.T * p.group - 1) / p.group);
+        top = -INFINITY;
+        sum = 0.0f;
         for (int j = u.j0; j < u.j1; ++j) {
             if (!__all_sync(0xffffffffu, cta.wait(kScores + stream, tiles_seen++ & 1)))
                 return;
             tc_fence_after();
             if (active) {
-                uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-                const bool tail = u.tail(j);
-                if (tail)
+                uint32_t s[2][32];
+                if (u.tail(j))  // what is hidden becomes -inf in its place
+#pragma unroll 1
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t seen = mask.seen(j * kTile + 32 * g - u.s.n);
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu))
+                            continue;
+                        tmem_load32(s[0], score_cols + 32 * g);
+                        tmem_wait_load(s[0]);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        seen[g] = u.s.end > 0 ? seen_word(p, u.s, q_row, j * kTile + 32 * g - u.s.n) : 0;
+                        for (int i = 0; i < 32; ++i)
+                            s[0][i] = seen >> i & 1 ? s[0][i] : 0xff800000u;
+                        tmem_store32(score_cols + 32 * g, s[0]);
+                        tmem_wait_store();
+                    }
                 // Scores are read twice, 32 columns at a time with the next 32
                 // on their way: once for the maximum and once for the weights,
                 // which take the place of scores already read.  Holding all
                 // 128 instead leaves too few registers for two CTAs.
-                uint32_t s[2][32];
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 tmem_load32(s[0], score_cols);
+#pragma unroll 1
+                for (int g = 0; g < 4; g += 2) {
+                    tmem_wait_load(s[0]);
+                    tmem_load32(s[1], score_cols + 32 * (g + 1));
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    tmem_wait_load(s[g & 1]);
-                    tmem_load32(s[(g + 1) & 1], score_cols + 32 * ((g + 1) & 3));
-                    if (tail) {
+                    for (int i = 0; i < 32; ++i)
+                        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[0][i]));
+                    tmem_wait_load(s[1]);
+                    tmem_load32(s[0], score_cols + 32 * (g + 2 & 3));
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            m[i & 3] = fmaxf(m[i & 3], seen[g] >> i & 1 ? __uint_as_float(s[g & 1][i])
-                                                                        : -INFINITY);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[g & 1][i]));
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[1][i]));
                 }
                 const float here = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 const bool moves = here > (top == -INFINITY ? top : top + slack);
@@ -731,6 +867,7 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                     top = here;
                     sum *= old;
                 }
+                tmem_wait_load(s[0]);
                 if (j != u.j0 && __any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
                     for (int g = 0; g < S::DP / 16; ++g) {
@@ -748,25 +885,29 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                 // Weights in 16 bits for the second product, as its operand
                 // type asks: a relative error of at most half an ulp each; the
                 // sum is of the unrounded ones.
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
+#pragma unroll 1
+                for (int g = 0; g < 4; g += 2) {
                     uint32_t w[16];
-                    tmem_wait_load(s[g & 1]);
-                    if (g < 3)
-                        tmem_load32(s[(g + 1) & 1], score_cols + 32 * (g + 1));
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float a = exp2_fast(fmaf(__uint_as_float(s[g & 1][2 * i]), c, -shift));
-                        float b = exp2_fast(fmaf(__uint_as_float(s[g & 1][2 * i + 1]), c, -shift));
-                        if (tail) {  // also where scale is 0 and the score is not finite
-                            a = seen[g] >> (2 * i) & 1 ? a : 0.0f;
-                            b = seen[g] >> (2 * i + 1) & 1 ? b : 0.0f;
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 0)
+                            tmem_load32(s[1], score_cols + 32 * (g + 1));
+                        else if (g == 0)
+                            tmem_load32(s[0], score_cols + 64);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float a = exp2_fast(fmaf(__uint_as_float(s[h][2 * i]), c, -shift));
+                            const float b = exp2_fast(fmaf(__uint_as_float(s[h][2 * i + 1]), c, -shift));
+                            part[2 * i & 3] += a;
+                            part[(2 * i + 1) & 3] += b;
+                            w[i] = pack16<S::BF16>(a, b);
                         }
-                        part[2 * i & 3] += a;
-                        part[(2 * i + 1) & 3] += b;
-                        w[i] = pack16<S::BF16>(a, b);
+                        tmem_store16(score_cols + 16 * (g + h), w);
+                        if (h == 0)
+                            tmem_wait_load(s[1]);
+                        else if (g == 0)
+                            tmem_wait_load(s[0]);
                     }
-                    tmem_store16(score_cols + 16 * g, w);
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
                 tmem_wait_store();
@@ -776,87 +917,8 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             if (lane == 0)
                 mbar_arrive(cta.bar(kWeights + stream));
         }
-
-        // The unit's end.  The next unit's query rows are on their way while
-        // the last product runs, and its first scores while the sums are read:
-        // they are not written again before this stream's next weights.
-        more = advance(after);
-        if (more)
-            fetch(after);
-        if (!__all_sync(0xffffffffu, cta.wait(kSums + stream, sums_seen++ & 1)))
-            return;
-        tc_fence_after();
-        if (more)
-            deliver();
-        if (!active)
-            continue;
-        const bool whole = u.whole(), real = mine < u.rows;
-        const bool bad = *(volatile int *)&cta.misc->bad[u.number & 7] == u.number + 1;
-        const int q_head = u.head * p.group + r - draft * p.group;
-        char *out = p.out + q_row * p.o_row + (int64_t)q_head * p.o_head;
-        float *part = part_of<S>(p, 2 * run + (u.j0 == 0 ? 1 : 0));
-        const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
-        if (real) {
-            if (!whole) {
-                part[mine] = top == -INFINITY ? top : top * c;
-                part[S::kUnitRows + mine] = sum;
-            } else if (p.lse) {
-                p.lse[q_row * p.q_heads + q_head] =
-                    top == -INFINITY && sum == 0.0f ? -INFINITY : top * scale + logf(sum);
-            }
-        }
-#pragma unroll 1
-        for (int g = 0; g < S::DP / 32; ++g) {
-            uint32_t o[32];
-            tmem_load32(o, sum_cols + 32 * g);
-            tmem_wait_load(o);
-            float x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                x[i] = __uint_as_float(o[i]);
-            if (!real)
-                continue;
-            if (bad) {
-                // Drafted values that are not finite, for the rows that see them.
-                const int from = max(u.j0 * kTile - u.s.n, 0);
-                const int to = min(u.j1 * kTile - u.s.n, u.s.T);
-                for (int d = from; d < to; ++d) {
-                    const int pos = u.s.n + d;
-                    if (!(seen_word(p, u.s, q_row, d) & 1u) || pos / p.c.page_tokens >= p.c.width)
-                        continue;
-                    const int page = p.c.table[(int64_t)u.s.slot * p.c.width + pos / p.c.page_tokens];
-                    if (page < 0 || page >= p.c.pages)
-                        continue;
-                    const char *v = p.c.pool[1] + page * p.c.page_stride +
-                                    pos % p.c.page_tokens * p.c.token_stride + u.head * p.c.head_stride;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * g + i < p.head_dim) {
-                            const uint32_t e = reinterpret_cast<const uint16_t *>(v)[32 * g + i];
-                            const uint32_t big = S::BF16 ? 0x7f80u : 0x7c00u, frac = S::BF16 ? 0x7fu : 0x3ffu;
-                            if ((e & big) == big)
-                                x[i] += e & frac ? NAN : e >> 15 ? -INFINITY : INFINITY;
-                        }
-                }
-            }
-            if (whole) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (32 * g + 8 * w < p.head_dim) {
-                        uint4 v;
-                        v.x = pack16<S::BF16>(x[8 * w] * inv, x[8 * w + 1] * inv);
-                        v.y = pack16<S::BF16>(x[8 * w + 2] * inv, x[8 * w + 3] * inv);
-                        v.z = pack16<S::BF16>(x[8 * w + 4] * inv, x[8 * w + 5] * inv);
-                        v.w = pack16<S::BF16>(x[8 * w + 6] * inv, x[8 * w + 7] * inv);
-                        *reinterpret_cast<uint4 *>(out + (32 * g + 8 * w) * 2) = v;
-                    }
-            } else {
-                float4 *to = reinterpret_cast<float4 *>(part + 2 * S::kUnitRows + mine * S::DP + 32 * g);
-#pragma unroll
-                for (int w = 0; w < 8; ++w)
-                    to[w] = make_float4(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]);
-            }
-        }
+        before = u;
+        begun = true;
     }
 }
 
@@ -899,8 +961,11 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if ((int)blockIdx.x < place.ctas) {
-        const Walk walk(p, S::kUnitRows, place, place.start(blockIdx.x + 1) - place.at);
+    const bool runs = (int)blockIdx.x < place.ctas;
+    const Walk walk(p, S::kUnitRows, place, runs ? place.start(blockIdx.x + 1) - place.at : 0);
+    if (threadIdx.x == 32 * (S::kSoftmaxWarps + 2))
+        note_cut<S>(p, place, walk);
+    if (runs) {
         // Registers a thread: launched with 168 (two streams) or 128; what the
         // last four warps give up is what the softmax warps take.
         //   128 * 72 + 256 * 216 = 384 * 168,   128 * 72 + 128 * 184 = 256 * 128
@@ -939,87 +1004,76 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of the units that run ends cut: CTA (x, y) looks at the end
-// of run x and takes rows kJoinRows y onwards of the unit it falls into, if
-// no earlier run ends in that unit.  A warp takes four rows side by side: their
-// loads do not wait for one another.
+// Joins the parts of the units that run ends cut: CTA (x, y) takes rows
+// kJoinRows y onwards of the unit whose first cut is run x + 1's start; a warp
+// per row, eight parts at a time, all of whose loads are under way before the
+// first is used.
 // ---------------------------------------------------------------------------
 template <class S>
-__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreePlan p, int grid)
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreePlan p, int ctas)
 {
-    __shared__ int64_t words[34];
     pdl_launch_dependents();
-    // Lengths and row starts were final before the launch ahead began: only
-    // the parts have to be waited for.
-    const Place at = find_run<kJoinThreads>(p, S::kUnitRows, grid, blockIdx.x + 1, words);
-    if ((int)blockIdx.x + 1 >= at.ctas)
-        return;
-    Walk walk(p, S::kUnitRows, at, 1);
-    Unit u;
-    walk.next(u);
-    const int64_t unit_start = at.at - u.j0, unit_end = unit_start + u.s.tiles;
-    const int row0 = blockIdx.y * kJoinRows, lane = threadIdx.x & 31;
-    if (u.j0 == 0 || row0 >= u.rows || at.start(blockIdx.x) > unit_start)
-        return;
-    // The unit's last run: no run is shorter than `each` tiles.
-    int last = blockIdx.x + 1;
-    while (last + 1 < at.ctas && at.start(last + 1) < unit_end)
-        ++last;
-    const int parts = last - (int)blockIdx.x + 1;
     pdl_wait_prerequisite();
-    constexpr int kPer = S::DP / 32, kSide = kJoinRows / (kJoinThreads / 32);
-    const int row = row0 + (threadIdx.x >> 5);  // and every eighth row after it
-    auto part = [&](int i) { return part_of<S>(p, 2 * ((int)blockIdx.x + i) + (i == 0)); };
-    float top[kSide], sum[kSide], x[kSide][kPer];
+    const Cut u = cuts_of<S>(p, ctas)[blockIdx.x + 1];
+    if ((int)blockIdx.y * kJoinRows >= u.rows)
+        return;
+    const int lane = threadIdx.x & 31, parts = u.parts;
+    constexpr int kPer = S::DP / 32, kSide = 8;
+    const float *first = part_of<S>(p, 2 * blockIdx.x + 1);  // the unit begins in this run
+    const int64_t pitch = 2 * part_floats(S::kUnitRows, S::DP);
+#pragma unroll 1
+    for (int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+         row < min((int)(blockIdx.y + 1) * kJoinRows, u.rows); row += kJoinThreads / 32) {
+        float top = -INFINITY, sum = 0.0f, x[kPer];
 #pragma unroll
-    for (int k = 0; k < kSide; ++k) {
-        top[k] = -INFINITY;
-        sum[k] = 0.0f;
+        for (int j = 0; j < kPer; ++j)
+            x[j] = 0.0f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < parts; i0 += kSide) {
+            float t[kSide], l[kSide], v[kSide][kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            x[k][i] = 0.0f;
-    }
-    for (int i = lane; i < parts; i += 32)
-#pragma unroll
-        for (int k = 0; k < kSide; ++k)
-            if (row + 8 * k < u.rows)
-                top[k] = fmaxf(top[k], part(i)[row + 8 * k]);
-#pragma unroll
-    for (int k = 0; k < kSide; ++k)
-        for (int o = 16; o; o /= 2)
-            top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], o));
-#pragma unroll 2
-    for (int i = 0; i < parts; ++i) {
-        const float *from = part(i);
-#pragma unroll
-        for (int k = 0; k < kSide; ++k)
-            if (row + 8 * k < u.rows) {
-                const float t = from[row + 8 * k];
-                const float f = t == top[k] ? 1.0f : t == -INFINITY ? 0.0f : exp2_fast(t - top[k]);
-                sum[k] = fmaf(from[S::kUnitRows + row + 8 * k], f, sum[k]);
-                const float *v = from + 2 * S::kUnitRows + (row + 8 * k) * S::DP + lane * kPer;
+            for (int i = 0; i < kSide; ++i) {
+                // Later parts lie in the slots of units begun before their run.
+                const float *from = first + (i0 + i) * pitch -
+                                    (i0 + i > 0 ? part_floats(S::kUnitRows, S::DP) : 0);
+                const bool is = i0 + i < parts;
+                t[i] = is ? from[row] : -INFINITY;
+                l[i] = is ? from[S::kUnitRows + row] : 0.0f;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    x[k][j] = fmaf(v[j], f, x[k][j]);
+                    v[i][j] = is ? from[2 * S::kUnitRows + row * S::DP + lane * kPer + j] : 0.0f;
             }
-    }
+            float most = top;
 #pragma unroll
-    for (int k = 0; k < kSide; ++k) {
-        if (row + 8 * k >= u.rows)
-            break;
-        const int r = u.r0 + row + 8 * k, draft = r / p.group;
-        const int q_head = u.head * p.group + r - draft * p.group;
-        const int64_t q_row = u.s.row0 + draft;
-        const float inv = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+            for (int i = 0; i < kSide; ++i)
+                most = fmaxf(most, t[i]);
+            const float old = top == most ? 1.0f : exp2_fast(top - most);
+            sum *= old;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                x[j] *= old;
+            top = most;
+#pragma unroll
+            for (int i = 0; i < kSide; ++i)
+                if (i0 + i < parts) {
+                    const float f = t[i] == top ? 1.0f : exp2_fast(t[i] - top);
+                    sum = fmaf(l[i], f, sum);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        x[j] = fmaf(v[i][j], f, x[j]);
+                }
+        }
+        const int r = u.r0 + row, draft = r / p.group, q_head = u.head * p.group + r - draft * p.group;
+        const int64_t q_row = u.row0 + draft;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         uint32_t *out = reinterpret_cast<uint32_t *>(p.out + q_row * p.o_row + (int64_t)q_head * p.o_head);
         if (lane * kPer < p.head_dim)
 #pragma unroll
             for (int j = 0; j < kPer / 2; ++j)
-                out[lane * kPer / 2 + j] = pack16<S::BF16>(x[k][2 * j] * inv, x[k][2 * j + 1] * inv);
+                out[lane * kPer / 2 + j] = pack16<S::BF16>(x[2 * j] * inv, x[2 * j + 1] * inv);
         if (p.lse && lane == 0)
-            p.lse[q_row * p.q_heads + q_head] = top[k] == -INFINITY && sum[k] == 0.0f
-                                                    ? -INFINITY
-                                                    : top[k] * 0.69314718055994530942f + logf(sum[k]);
+            p.lse[q_row * p.q_heads + q_head] =
+                top == -INFINITY && sum == 0.0f ? -INFINITY : top * 0.69314718055994530942f + logf(sum);
     }
 }
 
@@ -1120,8 +1174,9 @@ cudaError_t launch_shape(const TreePlan &p, int num_sms, bool pdl, cudaStream_t 
                               : launch_loads<S, false>(p, maps, ctas, pdl, stream);
     if (e != cudaSuccess || ctas < 2)
         return e;
-    return launch(k_tree_join<S>, dim3(ctas - 1, S::kUnitRows / kJoinRows), kJoinThreads, 0, pdl, stream,
-                  p, ctas);
+    const int rows = p.rows < S::kUnitRows / p.group ? p.rows * p.group : S::kUnitRows;
+    return launch(k_tree_join<S>, dim3(ctas - 1, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, pdl,
+                  stream, p, ctas);
 }
 
 template <int DP, bool BF16>
@@ -1136,8 +1191,9 @@ cudaError_t launch_dim(const TreePlan &p, int num_sms, bool pdl, cudaStream_t st
 
 uint64_t tree_workspace_bytes(int num_sms, int head_dim)
 {
-    // Two slots a run; half the runs with twice the rows for two streams.
-    return 4 * (uint64_t)num_sms * part_floats(kRowTile, head_dim <= 64 ? 64 : 128) * sizeof(float);
+    // Two slots a run, and a cut; two streams have half the runs and twice the rows.
+    return 4 * (uint64_t)num_sms * part_floats(kRowTile, head_dim <= 64 ? 64 : 128) * sizeof(float) +
+           2 * num_sms * sizeof(Cut);
 }
 
 cudaError_t launch_tree(const TreePlan &p, int num_sms, bool pdl, cudaStream_t stream)
