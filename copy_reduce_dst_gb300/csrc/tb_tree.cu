@@ -20,10 +20,11 @@ using namespace dev;
 // Work.  The query rows of a sequence that share a cache head are its (draft,
 // head of the group) pairs: T * group rows that read the same keys and values.
 // A unit is up to 128 of them per stream; its work is the sequence's tiles of
-// 128 positions.  The tiles of all units, one after another, are dealt to the
-// CTAs in equal runs, so a long sequence is split over many CTAs and short ones
-// share one, whatever their lengths; a unit cut by a run's end leaves partial
-// sums that k_tree_join puts together.
+// 128 positions, and kUnitCost tiles' worth of beginning and ending it.  The work
+// of all units, one after another, is dealt to the CTAs in equal runs, so a long
+// sequence is split over many CTAs and short ones share one, whatever their
+// lengths; a unit cut by a run's end leaves partial sums that k_tree_join puts
+// together.
 //
 // A stream is four warps that do the softmax of one 128-row tile.  The kernel
 // comes with one stream, two CTAs on an SM: one's softmax, first loads and last
@@ -36,7 +37,8 @@ constexpr int kRowTile = 128;    // rows of one matrix instruction
 constexpr int kLoadWarps = 3;    // load by threads, or ...
 constexpr int kFixWarps = 2;     // ... one asks for tiles and two look drafts over
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;    // rows of a unit one CTA of k_tree_join takes
+constexpr int kUnitCost = 2;     // what a unit costs besides its tiles, in tiles
+constexpr int kJoinRows = 8;     // rows of a unit one CTA of k_tree_join takes
 
 struct Seq {
     int slot, row0, T, n, end, tiles, units;  // units per cache head
@@ -59,7 +61,7 @@ __device__ __forceinline__ Seq seq_of(const TreePlan &p, int b, int unit_rows)
 __device__ __forceinline__ int64_t seq_work(const TreePlan &p, int b, int unit_rows)
 {
     const Seq s = seq_of(p, b, unit_rows);
-    return (int64_t)s.units * s.tiles * p.c.heads;
+    return (int64_t)s.units * p.c.heads * (s.tiles + kUnitCost);
 }
 
 // a / b for 0 <= a, 0 < b; 64-bit divisions cost hundreds of cycles.
@@ -69,12 +71,12 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
 }
 
 struct Place {
-    int64_t total;  // tiles of all units
-    int64_t at;     // the tile looked for
-    int64_t off;    // ... counted from the first of its sequence
+    int64_t total;  // work of all units
+    int64_t at;     // where the run begins
+    int64_t off;    // ... counted from the beginning of its sequence
     int b;
     int ctas;       // CTAs that get a run
-    int64_t each;   // tiles of every run; `more` of the runs have one on top
+    int64_t each;   // work of every run; `more` of the runs have one on top
     uint32_t more;
     // Start of run c.
     __device__ int64_t start(int c) const { return each * c + more * (uint32_t)c / (uint32_t)ctas; }
@@ -141,7 +143,9 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, int
     return r;
 }
 
-// A run's part of one unit: tiles j0 .. j1 - 1 for rows r0 .. r0 + rows - 1.
+// A run's part of one unit: tiles j0 .. j1 - 1 for rows r0 .. r0 + rows - 1.  A
+// unit's own cost comes before its first tile; a run that ends within that has
+// no part of the unit.
 struct Unit {
     Seq s;
     int number;  // within the run
@@ -154,36 +158,41 @@ struct Unit {
 struct Walk {
     const TreePlan &p;
     int64_t left;
-    int unit_rows, number, b, unit, j;  // unit: of the sequence, head by head
+    int unit_rows, number, b, unit, at;  // unit: of the sequence, head by head; at: within its work
     Seq s;
-    __device__ Walk(const TreePlan &plan, int rows, const Place &at, int64_t tiles)
-        : p(plan), left(tiles), unit_rows(rows), number(0), b(at.b)
+    __device__ Walk(const TreePlan &plan, int rows, const Place &place, int64_t work)
+        : p(plan), left(work), unit_rows(rows), number(0), b(place.b)
     {
         if (left > 0) {
             s = seq_of(p, b, unit_rows);
-            unit = (int)divide(at.off, s.tiles);
-            j = (int)(at.off - (int64_t)unit * s.tiles);
+            unit = (int)divide(place.off, s.tiles + kUnitCost);
+            at = (int)(place.off - (int64_t)unit * (s.tiles + kUnitCost));
         }
     }
     __device__ bool next(Unit &u)
     {
-        if (left <= 0)
-            return false;
-        while (unit >= s.units * p.c.heads) {
-            s = seq_of(p, ++b, unit_rows);  // there is one: tiles are left
-            unit = j = 0;
+        while (left > 0) {
+            if (unit >= s.units * p.c.heads) {
+                s = seq_of(p, ++b, unit_rows);  // there is one: work is left
+                unit = 0;
+                continue;
+            }
+            const int end = (int)min((int64_t)s.tiles + kUnitCost, at + left);
+            u.j0 = max(at - kUnitCost, 0);
+            u.j1 = end - kUnitCost;
+            left -= end - at;
+            at = 0;
+            const int mine = unit++;
+            if (u.j0 >= u.j1)
+                continue;
+            u.s = s;
+            u.number = number++;
+            u.head = mine / s.units;
+            u.r0 = (mine - u.head * s.units) * unit_rows;
+            u.rows = min(s.T * p.group - u.r0, unit_rows);
+            return true;
         }
-        u.s = s;
-        u.number = number++;
-        u.head = unit / s.units;
-        u.r0 = (unit - u.head * s.units) * unit_rows;
-        u.rows = min(s.T * p.group - u.r0, unit_rows);
-        u.j0 = j;
-        u.j1 = (int)min((int64_t)s.tiles, j + left);
-        left -= u.j1 - u.j0;
-        j = 0;
-        ++unit;
-        return true;
+        return false;
     }
 };
 
@@ -623,7 +632,7 @@ __device__ void note_cut(const TreePlan &p, const Place &place, Walk walk)
     Cut cut{};
     Unit u;
     if ((int)blockIdx.x < place.ctas && walk.next(u) && u.j0 > 0) {
-        const int64_t begin = place.at - u.j0, end = begin + u.s.tiles;
+        const int64_t begin = place.at - u.j0, end = begin + u.s.tiles;  // of its tiles
         if (place.start(blockIdx.x - 1) <= begin) {
             int last = (int)min(divide(end * place.ctas, place.total), (int64_t)place.ctas - 1);
             while (place.start(last) >= end)
