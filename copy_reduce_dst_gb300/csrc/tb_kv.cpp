@@ -97,6 +97,8 @@ int view_of(tb_ctx *ctx, const tb_kv_cache *cache, bool pools, bool table, const
         // Positions of a slot are counted in 32 bits.
         if (c.table_width > (1 << 30) / c.page_tokens)
             return fail(ctx, TB_ENOTSUP, "%s: table_width * page_tokens exceeds 2^30", who);
+        if (c.pages > 1 << 30 || c.slots > INT_MAX / c.table_width)
+            return fail(ctx, TB_ENOTSUP, "%s: more than 2^30 pages or 2^31 - 1 table entries", who);
         v.table = c.table;
         v.held = c.held;
         v.lens = c.lens;

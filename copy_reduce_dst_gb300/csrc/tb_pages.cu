@@ -54,7 +54,7 @@ __device__ __forceinline__ Runs page_runs(const KvView &c, uint32_t tokens)
     return r;
 }
 
-// One page of one layer by a whole CTA, 16 bytes a thread and step.
+// One page of one layer by a whole CTA, four 16-byte loads a thread in flight.
 __device__ __forceinline__ void copy_page(const KvView &c, char *pool, int32_t src, int32_t dst,
                                           uint32_t tokens)
 {
@@ -62,16 +62,37 @@ __device__ __forceinline__ void copy_page(const KvView &c, char *pool, int32_t s
     const uint32_t per_run = r.bytes / 16, total = r.n1 * r.n2 * per_run;
     const char *from = pool + src * c.page_stride;
     char *to = pool + dst * c.page_stride;
-    for (uint32_t i = threadIdx.x; i < total; i += blockDim.x) {
+    auto place = [&](uint32_t i) {
+        if (r.n1 * r.n2 == 1)
+            return (int64_t)i * 16;
         const uint32_t run = i / per_run;
-        const int64_t at = (run / r.n2) * r.s1 + (run % r.n2) * r.s2 + (int64_t)(i % per_run) * 16;
-        *reinterpret_cast<uint4 *>(to + at) = *reinterpret_cast<const uint4 *>(from + at);
+        return (run / r.n2) * r.s1 + (run % r.n2) * r.s2 + (int64_t)(i - run * per_run) * 16;
+    };
+    for (uint32_t i = threadIdx.x; i < total; i += 4 * blockDim.x) {
+        uint4 v[4];
+        int64_t at[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * blockDim.x < total) {
+                at[u] = place(i + u * blockDim.x);
+                v[u] = *reinterpret_cast<const uint4 *>(from + at[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i + u * blockDim.x < total)
+                *reinterpret_cast<uint4 *>(to + at[u]) = v[u];
     }
 }
 
 __device__ __forceinline__ bool is_page(const KvView &c, int32_t p)
 {
     return p >= 0 && p < c.pages;
+}
+
+// Pool of a layer's keys (even lanes) or values (odd).
+__device__ __forceinline__ char *pool_of(const KvView &c, int32_t lane)
+{
+    return (lane & 1 ? c.pool[1] : c.pool[0]) + (lane >> 1) * c.layer_stride;
 }
 
 __global__ void __launch_bounds__(kPageThreads)
@@ -81,12 +102,12 @@ __global__ void __launch_bounds__(kPageThreads)
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
-        const int64_t i = j / (2 * c.layers);
-        const int32_t lane = (int32_t)(j % (2 * c.layers));
+        const int64_t i = j >> 32 ? j / (2 * c.layers) : (uint32_t)j / (uint32_t)(2 * c.layers);
+        const int32_t lane = (int32_t)(j - i * (2 * c.layers));
         const int32_t s = src[i], d = dst[i];
         const int32_t t = tokens ? min(max(tokens[i], 0), c.page_tokens) : c.page_tokens;
         if (is_page(c, s) && is_page(c, d) && s != d && t > 0)
-            copy_page(c, c.pool[lane & 1] + (lane >> 1) * c.layer_stride, s, d, (uint32_t)t);
+            copy_page(c, pool_of(c, lane), s, d, (uint32_t)t);
     }
 }
 
@@ -125,101 +146,232 @@ __device__ __forceinline__ int pages_for(int tokens, int page_tokens)
     return tokens / page_tokens + (tokens % page_tokens != 0);
 }
 
-// Free pages of the pool.
-__device__ int count_free(const KvView &c, int *warp_sums)
+// ---------------------------------------------------------------------------
+// Handing out pages.  "The lowest free pages" needs a count of the free pages
+// before each one: the pool's counts are split over the CTAs of one cluster
+// (their SMs read together; totals meet in distributed shared memory, so no
+// scratch memory is needed), and each warp counts, then hands out, a run of
+// them.  The counts are read again for the second pass: no page before its own
+// reader has handed it out changes between the two.
+// ---------------------------------------------------------------------------
+constexpr int kCluster = 16;       // CTAs for a large pool; one for a small one
+constexpr int kClusterPages = 16384;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+__device__ __forceinline__ uint32_t cluster_rank()
 {
-    int mine = 0, total;
-    for (int p = threadIdx.x; p < c.pages; p += blockDim.x)
-        mine += c.refs[p] == 0;
-    scan_before(mine, warp_sums, total);
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// All threads of the cluster; orders their memory accesses before and after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Writes a word of the same shared variable in CTA `rank`.
+__device__ __forceinline__ void store_remote(int *local, uint32_t rank, int value)
+{
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(remote)
+                 : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(value) : "memory");
+}
+
+struct FreeCount {
+    int cta[kCluster];      // free pages in each CTA's share
+    int warp[kPlanWarps];   // ... in each warp's, this CTA
+};
+
+// This warp's share of the pages, in multiples of 128.
+__device__ __forceinline__ void page_share(const KvView &c, int &from, int &to)
+{
+    const int shares = (int)cluster_size() * kPlanWarps;
+    const int mine = (int)cluster_rank() * kPlanWarps + (int)(threadIdx.x >> 5);
+    const int blocks = c.pages / 128 + (c.pages % 128 != 0);
+    const int each = blocks / shares, more = blocks % shares;
+    const int first = each * mine + min(mine, more), count = each + (mine < more);
+    from = min(first * 128, c.pages);  // pages <= 2^30
+    to = min(from + count * 128, c.pages);
+}
+
+// Which of pages p .. p + 3 are free, as bits; one 16-byte load.
+__device__ __forceinline__ uint32_t free_bits(const KvView &c, int p, int to)
+{
+    if (p + 4 <= to && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
+        const int4 r = *reinterpret_cast<const int4 *>(c.refs + p);
+        return (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
+    }
+    uint32_t bits = 0;
+    for (int k = 0; k < 4; ++k)
+        if (p + k < to && c.refs[p + k] == 0)
+            bits |= 1u << k;
+    return bits;
+}
+
+// Free pages of the pool; all threads of the cluster call it, after a
+// cluster_sync that says that every CTA runs.
+__device__ int count_free(const KvView &c, FreeCount &f)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int from, to, mine = 0;
+    page_share(c, from, to);
+#pragma unroll 4
+    for (int p = from + lane * 4; p < to; p += 128)
+        mine += __popc(free_bits(c, p, to));
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0)
+        f.warp[warp] = mine;
+    __syncthreads();
+    if (warp == 0) {
+        const int sum = __reduce_add_sync(0xffffffffu, f.warp[lane]);
+        if (lane < (int)cluster_size())
+            store_remote(&f.cta[cluster_rank()], lane, sum);
+    }
+    cluster_sync();
+    int total = 0;
+    for (uint32_t r = 0; r < cluster_size(); ++r)
+        total += f.cta[r];
     return total;
 }
 
-// Calls take(rank, page) for the `wanted` lowest free pages, in any order.
+// Calls take(rank, page) for the `wanted` lowest free pages, after count_free.
 template <class Take>
-__device__ void take_free(const KvView &c, int wanted, int *warp_sums, Take take)
+__device__ void take_free(const KvView &c, const FreeCount &f, int wanted, Take take)
 {
-    int rank = 0;
-    for (int base = 0; base < c.pages && rank < wanted; base += blockDim.x) {
-        const int p = base + (int)threadIdx.x;
-        const int is_free = p < c.pages && c.refs[p] == 0;
-        int total;
-        const int mine = rank + scan_before(is_free, warp_sums, total);
-        if (is_free && mine < wanted)
-            take(mine, p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int rank = 0, from, to;
+    for (uint32_t r = 0; r < cluster_rank(); ++r)
+        rank += f.cta[r];
+    for (int w = 0; w < warp; ++w)
+        rank += f.warp[w];
+    page_share(c, from, to);
+    const int end = rank + f.warp[warp];
+    for (int base = from; base < to && rank < wanted && rank < end; base += 128) {
+        const uint32_t bits = free_bits(c, base + lane * 4, to);
+        int before = __popc(bits);
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d)
+                before += y;
+        }
+        const int total = __shfl_sync(0xffffffffu, before, 31);
+        int mine = rank + before - __popc(bits);
+        for (int k = 0; k < 4; ++k)
+            if (bits >> k & 1) {
+                if (mine < wanted)
+                    take(mine, base + lane * 4 + k);
+                ++mine;
+            }
         rank += total;
     }
+}
+
+// The last of n ascending entries (the first is 0) that is <= x.
+__device__ __forceinline__ int last_at_most(const int *v, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (v[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
     k_kv_resize(const KvView c, const int32_t *capacity, int32_t *status)
 {
-    extern __shared__ int first_rank[];  // [slots]: rank of the first page each slot takes
+    extern __shared__ int shared[];
+    int *first_new = shared;              // [slots] pages that the slots before it take
+    int *first_gone = shared + c.slots;   // [slots] ... give back
+    int *held = shared + 2 * c.slots;     // [slots]
     __shared__ int warp_sums[33];
+    __shared__ FreeCount found;
     __shared__ int bad;
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     if (threadIdx.x == 0)
         bad = 0;
-    __syncthreads();
-    int wanted = 0;
+    cluster_sync();
+    int wanted = 0, gone = 0;
     for (int base = 0; base < c.slots; base += blockDim.x) {
         const int s = base + (int)threadIdx.x;
-        int grow = 0;
-        if (s < c.slots && capacity[s] >= 0) {
-            const int cap = capacity[s], held = min(max(c.held[s], 0), c.width);
-            const int need = pages_for(cap, c.page_tokens);
-            if (need > c.width)
-                bad = 1;
-            // The last page kept is written again past the cut: not if it is shared.
-            if (cap < c.lens[s] && cap % c.page_tokens && need <= held) {
-                const int p = c.table[(int64_t)s * c.width + need - 1];
-                if (is_page(c, p) && c.refs[p] > 1)
+        int grow = 0, shrink = 0;
+        if (s < c.slots) {
+            const int cap = capacity[s], has = min(max(c.held[s], 0), c.width), length = c.lens[s];
+            held[s] = has;
+            if (cap >= 0) {
+                const int need = pages_for(cap, c.page_tokens);
+                if (need > c.width)
                     bad = 1;
+                // The last page kept is written again past the cut: not if it is shared.
+                if (cap < length && cap % c.page_tokens && need <= has) {
+                    const int p = c.table[(int64_t)s * c.width + need - 1];
+                    if (is_page(c, p) && c.refs[p] > 1)
+                        bad = 1;
+                }
+                grow = min(max(need - has, 0), c.width);
+                shrink = max(has - need, 0);
             }
-            grow = max(need - held, 0);
         }
         int total;
-        const int before = scan_before(min(grow, c.width), warp_sums, total);
+        const int before = scan_before(grow, warp_sums, total);
         if (s < c.slots)
-            first_rank[s] = wanted + before;
+            first_new[s] = wanted + before;
         wanted += total;
+        const int before_gone = scan_before(shrink, warp_sums, total);
+        if (s < c.slots)
+            first_gone[s] = gone + before_gone;
+        gone += total;
     }
-    const int missing = wanted ? max(wanted - count_free(c, warp_sums), 0) : 0;
     __syncthreads();
+    int missing = 0;
+    if (wanted)
+        missing = max(wanted - count_free(c, found), 0);
     const int verdict = bad ? -1 : missing;
-    if (threadIdx.x == 0)
+    if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
+    if (!verdict && wanted)
+        take_free(c, found, wanted, [&](int rank, int p) {
+            const int s = last_at_most(first_new, c.slots, rank);
+            c.table[(int64_t)s * c.width + held[s] + rank - first_new[s]] = p;
+            c.refs[p] = 1;
+        });
+    // Pages are given back after every CTA has looked for free ones, and
+    // nothing is written before all have read held and lens.
+    cluster_sync();
     if (verdict)
         return;
-    take_free(c, wanted, warp_sums, [&](int rank, int p) {
-        int lo = 0, hi = c.slots;  // the last slot whose first rank is <= rank
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (first_rank[mid] <= rank)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int held = min(max(c.held[lo], 0), c.width);
-        c.table[(int64_t)lo * c.width + held + rank - first_rank[lo]] = p;
-        c.refs[p] = 1;
-    });
-    __syncthreads();
-    for (int s = threadIdx.x >> 5; s < c.slots; s += blockDim.x >> 5) {
+    const int threads = (int)cluster_size() * kPlanThreads;
+    const int mine = (int)cluster_rank() * kPlanThreads + (int)threadIdx.x;
+#pragma unroll 4
+    for (int i = mine; i < gone; i += threads) {
+        const int s = last_at_most(first_gone, c.slots, i);
+        const int kept = pages_for(capacity[s], c.page_tokens);
+        int32_t *entry = c.table + (int64_t)s * c.width + kept + i - first_gone[s];
+        const int p = *entry;
+        if (is_page(c, p))
+            atomicSub(c.refs + p, 1);
+        *entry = -1;
+    }
+    for (int s = mine; s < c.slots; s += threads) {
         const int cap = capacity[s];
-        if (cap < 0)
-            continue;
-        const int held = min(max(c.held[s], 0), c.width), need = pages_for(cap, c.page_tokens);
-        for (int j = need + (int)(threadIdx.x & 31); j < held; j += 32) {
-            int32_t *entry = c.table + (int64_t)s * c.width + j;
-            if (is_page(c, *entry))
-                atomicSub(c.refs + *entry, 1);
-            *entry = -1;
-        }
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            c.held[s] = need;
+        if (cap >= 0) {
+            c.held[s] = pages_for(cap, c.page_tokens);
             c.lens[s] = min(c.lens[s], cap);
         }
     }
@@ -229,9 +381,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Fork
 // ---------------------------------------------------------------------------
 
-// Decides which children take a fresh page for the part-filled one, takes
-// those pages and enters them in the output table; the launch after it does
-// the rest by what it finds there.
+// Decides which children take a fresh page for the part-filled one and takes
+// those pages.  It enters the page that holds the part-filled one's tokens in
+// the output row of every slot that does not simply go on: the launch after it
+// copies where that is another page, and leaves the entry alone.
 __global__ void __launch_bounds__(kPlanThreads)
     k_fork_plan(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *status)
 {
@@ -239,6 +392,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     int *heir = shared;               // [slots]: -1: the slot goes on; else its lowest child
     int *needy = shared + c.slots;    // slots that take a fresh page, in order
     __shared__ int warp_sums[33];
+    __shared__ FreeCount found;
     __shared__ int bad;
     pdl_launch_dependents();
     pdl_wait_prerequisite();
@@ -246,7 +400,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         bad = 0;
     for (int s = threadIdx.x; s < c.slots; s += blockDim.x)
         heir[s] = INT32_MAX;
-    __syncthreads();
+    cluster_sync();
     for (int s = threadIdx.x; s < c.slots; s += blockDim.x) {
         const int p = parents[s];
         if (p >= c.slots)
@@ -261,8 +415,15 @@ __global__ void __launch_bounds__(kPlanThreads)
         int takes = 0;
         if (s < c.slots) {
             const int p = parents[s];
-            takes = p >= 0 && p < c.slots && p != s && heir[p] != s && c.lens[p] > 0 &&
-                    c.lens[p] % c.page_tokens != 0 && c.lens[p] / c.page_tokens < c.width;
+            if (p >= 0 && p < c.slots && p != s) {
+                const int length = c.lens[p], full = length / c.page_tokens;
+                takes = length > 0 && length % c.page_tokens != 0 && full < c.width;
+                if (takes && heir[p] == s) {
+                    takes = 0;
+                    if (cluster_rank() == 0)
+                        table_out[(int64_t)s * c.width + full] = c.table[(int64_t)p * c.width + full];
+                }
+            }
         }
         int total;
         const int before = scan_before(takes, warp_sums, total);
@@ -270,33 +431,56 @@ __global__ void __launch_bounds__(kPlanThreads)
             needy[wanted + before] = s;
         wanted += total;
     }
-    const int missing = wanted ? max(wanted - count_free(c, warp_sums), 0) : 0;
     __syncthreads();
+    int missing = 0;
+    if (wanted)
+        missing = max(wanted - count_free(c, found), 0);
     const int verdict = bad ? -1 : missing;
-    if (threadIdx.x == 0)
+    if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
-    if (verdict)
-        return;
-    take_free(c, wanted, warp_sums, [&](int rank, int page) {
-        const int s = needy[rank], p = parents[s];
-        table_out[(int64_t)s * c.width + c.lens[p] / c.page_tokens] = page;
-        c.refs[page] = 1;
-    });
+    if (!verdict && wanted)
+        take_free(c, found, wanted, [&](int rank, int page) {
+            const int s = needy[rank], p = parents[s];
+            table_out[(int64_t)s * c.width + c.lens[p] / c.page_tokens] = page;
+            c.refs[page] = 1;
+        });
 }
 
-// The rows, counts and lengths after the plan: CTA (x, s) does entries
-// x * kPageThreads .. of slot s's old row and of its new one.
+// The rest of the fork.  Blocks below row_blocks: entries of slot s's old row
+// (counts) and of its new one; the others: the part-filled page of a child that
+// took a fresh one, kTailLanes layers' keys or values each.
+constexpr int kTailLanes = 4;
+
 __global__ void __launch_bounds__(kPageThreads)
-    k_fork_rows(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *held_out,
-                int32_t *lens_out, const int32_t *status)
+    k_fork_rest(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *held_out,
+                int32_t *lens_out, const int32_t *status, int row_blocks, int blocks_per_row)
 {
     __shared__ int children, others;  // children of slot s; its parent's lowest child, -1: itself
     pdl_launch_dependents();
     pdl_wait_prerequisite();
-    const int s = blockIdx.y, j = blockIdx.x * blockDim.x + threadIdx.x;
+    const bool refused = *status != 0;
+    if ((int)blockIdx.x >= row_blocks) {
+        const int lanes = 2 * c.layers, groups = (lanes + kTailLanes - 1) / kTailLanes;
+        const int s = (blockIdx.x - row_blocks) / groups;
+        const int first = (blockIdx.x - row_blocks) % groups * kTailLanes;
+        const int p = parents[s];
+        if (refused || p < 0 || p == s)
+            return;
+        const int length = c.lens[p], full = length / c.page_tokens, tail = length % c.page_tokens;
+        if (length <= 0 || tail == 0 || full >= c.width)
+            return;
+        const int from = c.table[(int64_t)p * c.width + full];
+        const int to = table_out[(int64_t)s * c.width + full];
+        if (is_page(c, from) && is_page(c, to) && from != to)
+            for (int lane = first; lane < min(first + kTailLanes, lanes); ++lane)
+                copy_page(c, pool_of(c, lane), from, to, (uint32_t)tail);
+        return;
+    }
+    const int s = blockIdx.x / blocks_per_row;
+    const int j = blockIdx.x % blocks_per_row * blockDim.x + threadIdx.x;
     const int64_t row = (int64_t)s * c.width;
     const int p = parents[s];
-    if (*status) {
+    if (refused) {
         if (j < c.width)
             table_out[row + j] = c.table[row + j];
         if (j == 0) {
@@ -328,32 +512,12 @@ __global__ void __launch_bounds__(kPageThreads)
     const int length = p >= 0 ? c.lens[p] : 0, full = length / c.page_tokens;
     const bool tail = length % c.page_tokens != 0;
     const int keeps = p < 0 ? 0 : inherits ? min(c.held[p], c.width) : min(full + tail, c.width);
-    if (j < c.width && !(p >= 0 && !inherits && tail && j == full))
+    if (j < c.width && !(p >= 0 && p != s && tail && j == full))  // the plan's entry
         table_out[row + j] = j < keeps ? c.table[(int64_t)p * c.width + j] : -1;
     if (j == 0) {
         held_out[s] = keeps;
         lens_out[s] = length;
     }
-}
-
-// The part-filled pages of the children that took a fresh one.
-__global__ void __launch_bounds__(kPageThreads)
-    k_fork_tails(const KvView c, const int32_t *parents, const int32_t *table_out,
-                 const int32_t *status)
-{
-    pdl_launch_dependents();
-    pdl_wait_prerequisite();
-    const int s = blockIdx.x / (2 * c.layers), lane = blockIdx.x % (2 * c.layers);
-    const int p = parents[s];
-    if (*status || p < 0 || p == s)
-        return;
-    const int length = c.lens[p], full = length / c.page_tokens, tail = length % c.page_tokens;
-    if (length <= 0 || tail == 0 || full >= c.width)
-        return;
-    const int from = c.table[(int64_t)p * c.width + full];
-    const int to = table_out[(int64_t)s * c.width + full];
-    if (is_page(c, from) && is_page(c, to) && from != to)
-        copy_page(c, c.pool[lane & 1] + (lane >> 1) * c.layer_stride, from, to, (uint32_t)tail);
 }
 
 // ---------------------------------------------------------------------------
@@ -363,14 +527,16 @@ __global__ void __launch_bounds__(kPageThreads)
 // one column through the slot's list.  It reads kAhead tokens, then writes
 // them: every later source lies past every destination written so far (keep
 // ascends, so keep[i] >= i), so no column needs another's progress.
-constexpr int kAhead = 8;
+constexpr int kAhead = 16;
+constexpr int kCompactBlock = 128;   // list entries looked up at a time
+constexpr int kCompactThreads = 64;  // small CTAs: the columns spread over more SMs
 
-__global__ void __launch_bounds__(kPageThreads)
+__global__ void __launch_bounds__(kCompactThreads)
     k_kv_compact(const KvView c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
                  const int32_t *count, int32_t *status)
 {
     __shared__ int verdict, skip;
-    __shared__ int64_t from[kPageThreads], to[kPageThreads];
+    __shared__ int64_t from[kCompactBlock], to[kCompactBlock];
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     const int s = blockIdx.y, n = count[s], P = c.page_tokens;
@@ -391,6 +557,7 @@ __global__ void __launch_bounds__(kPageThreads)
     if (n > keep_stride || first < 0 || first + n > room)
         verdict = 2;
     else
+#pragma unroll 4
         for (int i = threadIdx.x; i < n; i += blockDim.x) {
             const int k = list[i];
             if (k < 0 || first + k >= room || (i > 0 && list[i - 1] >= k) ||
@@ -418,17 +585,16 @@ __global__ void __launch_bounds__(kPageThreads)
     const int64_t total = 2ll * c.layers * c.heads * cols;
     char *base = nullptr;
     if (col < total) {
-        const int64_t pl = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
-        base = c.pool[pl & 1] + (pl >> 1) * c.layer_stride + in / cols * c.head_stride +
-               in % cols * 16;
+        const int64_t lane = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
+        base = pool_of(c, (int32_t)lane) + in / cols * c.head_stride + in % cols * 16;
     }
-    for (int b = skip; b < n; b += kPageThreads) {
-        const int here = min(n - b, kPageThreads), i = b + (int)threadIdx.x;
+    for (int b = skip; b < n; b += kCompactBlock) {
+        const int here = min(n - b, kCompactBlock);
         __syncthreads();
-        if ((int)threadIdx.x < here) {
-            const int64_t f = first + list[i], t = first + i;
-            from[threadIdx.x] = row[f / P] * c.page_stride + f % P * c.token_stride;
-            to[threadIdx.x] = row[t / P] * c.page_stride + t % P * c.token_stride;
+        for (int k = threadIdx.x; k < here; k += kCompactThreads) {
+            const int64_t f = first + list[b + k], t = first + b + k;
+            from[k] = row[f / P] * c.page_stride + f % P * c.token_stride;
+            to[k] = row[t / P] * c.page_stride + t % P * c.token_stride;
         }
         __syncthreads();
         if (!base)
@@ -451,19 +617,22 @@ __global__ void __launch_bounds__(kPageThreads)
 // Launches
 // ---------------------------------------------------------------------------
 template <class... Args>
-cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, bool pdl,
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster, bool pdl,
                    cudaStream_t stream, Args... args)
 {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -476,14 +645,34 @@ cudaError_t launch_copy_pages(const KvView &c, const int32_t *src, const int32_t
     (void)num_sms;
     const int64_t jobs = 2ll * c.layers * n;
     const unsigned grid = (unsigned)(jobs < (1 << 30) ? jobs : 1 << 30);
-    return launch(k_copy_pages, dim3(grid), kPageThreads, 0, pdl, stream, c, src, dst, tokens, jobs);
+    return launch(k_copy_pages, dim3(grid), kPageThreads, 0, 1, pdl, stream, c, src, dst, tokens, jobs);
 }
+
+namespace {
+
+// Launches a kernel that hands out pages: its CTAs are one cluster.
+template <class... Args>
+cudaError_t launch_plan(void (*kernel)(Args...), const KvView &c, size_t smem, bool pdl,
+                        cudaStream_t stream, Args... args)
+{
+    const int cluster = c.pages > kClusterPages ? kCluster : 1;
+    cudaError_t e = cudaSuccess;
+    if (cluster > 8)
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && smem > 40 * 1024)  // beside the static shared memory
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)smem);
+    if (e != cudaSuccess)
+        return e;
+    return launch(kernel, dim3(cluster), kPlanThreads, smem, cluster, pdl, stream, args...);
+}
+
+}  // namespace
 
 cudaError_t launch_kv_resize(const KvView &c, const int32_t *capacity, int32_t *status, bool pdl,
                              cudaStream_t stream)
 {
-    return launch(k_kv_resize, dim3(1), kPlanThreads, c.slots * sizeof(int), pdl, stream, c,
-                  capacity, status);
+    return launch_plan(k_kv_resize, c, 3 * c.slots * sizeof(int), pdl, stream, c, capacity, status);
 }
 
 cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *table_out,
@@ -491,24 +680,14 @@ cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *tab
                            bool pdl, cudaStream_t stream)
 {
     (void)num_sms;
-    const size_t smem = 2 * c.slots * sizeof(int);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            (const void *)k_fork_plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
-    }
-    cudaError_t e = launch(k_fork_plan, dim3(1), kPlanThreads, smem, pdl, stream, c, parents,
-                           table_out, status);
+    const cudaError_t e = launch_plan(k_fork_plan, c, 2 * c.slots * sizeof(int), pdl, stream, c, parents,
+                                      table_out, status);
     if (e != cudaSuccess)
         return e;
-    e = launch(k_fork_rows, dim3((c.width + kPageThreads - 1) / kPageThreads, c.slots),
-               kPageThreads, 0, pdl, stream, c, parents, table_out, held_out, lens_out,
-               (const int32_t *)status);
-    if (e != cudaSuccess)
-        return e;
-    return launch(k_fork_tails, dim3((unsigned)(2ll * c.layers * c.slots)), kPageThreads, 0, pdl,
-                  stream, c, parents, (const int32_t *)table_out, (const int32_t *)status);
+    const int per_row = (c.width + kPageThreads - 1) / kPageThreads, rows = c.slots * per_row;
+    const int groups = (2 * c.layers + kTailLanes - 1) / kTailLanes;
+    return launch(k_fork_rest, dim3((unsigned)rows + (unsigned)(c.slots * groups)), kPageThreads, 0, 1, pdl,
+                  stream, c, parents, table_out, held_out, lens_out, (const int32_t *)status, rows, per_row);
 }
 
 cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32_t *keep,
@@ -516,8 +695,8 @@ cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32
                               bool pdl, cudaStream_t stream)
 {
     const int64_t cols = 2ll * c.layers * c.heads * (c.row_bytes / 16);
-    return launch(k_kv_compact, dim3((unsigned)((cols + kPageThreads - 1) / kPageThreads), c.slots),
-                  kPageThreads, 0, pdl, stream, c, start, keep, keep_stride, count, status);
+    return launch(k_kv_compact, dim3((unsigned)((cols + kCompactThreads - 1) / kCompactThreads), c.slots),
+                  kCompactThreads, 0, 1, pdl, stream, c, start, keep, keep_stride, count, status);
 }
 
 }  // namespace tb

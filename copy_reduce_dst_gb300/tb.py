@@ -394,13 +394,19 @@ def _kv_dtype(t) -> int:
     raise TypeError(f"no cache of {name}")
 
 
-def _int32(t, what: str, *shape: int | None):
-    """Checks a dense int32 device tensor's shape (None: any size)."""
+_INT32 = set()  # the tensor library's int32, once seen: comparing it is cheaper than its name
+
+
+def _int32(t, what: str, shape: tuple) -> int:
+    """Address of a dense int32 device tensor of this shape (None: any size)."""
+    if t is not None and t.dtype in _INT32 and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t is None or _dtype_name(t) != "int32" or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous int32 CUDA tensor")
     if len(t.shape) != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
-    return t
+    _INT32.add(t.dtype)
+    return t.data_ptr()
 
 
 class KvCache:
@@ -409,8 +415,13 @@ class KvCache:
     def __init__(self, struct: KvCacheStruct, tensors: tuple):
         self.struct = struct
         self.ref = ct.byref(struct)
+        self.ptr = ct.pointer(struct)
         self.tensors = tensors
-        self.name = _dtype_name(tensors[0]) if tensors[0] is not None else ""
+        self.dtype = tensors[0].dtype if tensors[0] is not None else None
+        # What the calls check their lists against, as plain values.
+        self.per_slot = (struct.slots,)
+        self.table_shape = (struct.slots, struct.table_width)
+        self.head_dim = struct.head_dim
 
 
 def kv_cache(k=None, v=None, table=None, held=None, lens=None, refs=None, layout: str = "NHD",
@@ -447,13 +458,11 @@ def kv_cache(k=None, v=None, table=None, held=None, lens=None, refs=None, layout
     else:
         s.page_tokens = page_tokens or 0
     if table is not None:
-        _int32(table, "table", None, None)
+        s.table = _int32(table, "table", (None, None))
         s.slots, s.table_width = table.shape
-        _int32(held, "held", s.slots)
-        _int32(lens, "lens", s.slots)
-        _int32(refs, "refs", s.pages if k is not None else None)
+        s.held, s.lens = _int32(held, "held", (s.slots,)), _int32(lens, "lens", (s.slots,))
+        s.refs = _int32(refs, "refs", (s.pages if k is not None else None,))
         s.pages = refs.shape[0]
-        s.table, s.held, s.lens, s.refs = (t.data_ptr() for t in (table, held, lens, refs))
     return KvCache(s, (k, v, table, held, lens, refs))
 
 
@@ -629,46 +638,40 @@ class Context:
                       stream=None):
         """tb_kv_copy_pages: page src[i] to page dst[i] in every layer, keys
         and values, for the first n entries of the lists (default: all)."""
-        _int32(src, "src", None)
-        _int32(dst, "dst", None)
+        s, d, m = _int32(src, "src", src.shape[:1]), _int32(dst, "dst", dst.shape[:1]), 0
         most = min(src.shape[0], dst.shape[0])
         if tokens is not None:
-            most = min(most, _int32(tokens, "tokens", None).shape[0])
+            m = _int32(tokens, "tokens", tokens.shape[:1])
+            most = min(most, tokens.shape[0])
         if n is None:
             n = most
         elif n > most:
             raise ValueError(f"n is {n}, the shortest list has {most} entries")
-        self._ok(lib.tb_kv_copy_pages(self._h, cache.ref, src.data_ptr(), dst.data_ptr(),
-                                      addr(tokens), n, stream_handle(stream)), "tb_kv_copy_pages")
+        self._ok(lib.tb_kv_copy_pages(self._h, cache.ref, s, d, m, n, stream_handle(stream)),
+                 "tb_kv_copy_pages")
 
     def kv_resize(self, cache: KvCache, capacity, status, stream=None):
         """tb_kv_resize: each slot gets exactly the pages of capacity[s] tokens."""
-        _int32(capacity, "capacity", cache.struct.slots)
-        _int32(status, "status", 1)
-        self._ok(lib.tb_kv_resize(self._h, cache.ref, capacity.data_ptr(), status.data_ptr(),
-                                  stream_handle(stream)), "tb_kv_resize")
+        self._ok(lib.tb_kv_resize(self._h, cache.ref, _int32(capacity, "capacity", cache.per_slot),
+                                  _int32(status, "status", (1,)), stream_handle(stream)),
+                 "tb_kv_resize")
 
     def kv_fork(self, cache: KvCache, parents, table_out, held_out, lens_out, status, stream=None):
         """tb_kv_fork: slot s becomes the sequence of slot parents[s]."""
-        slots = cache.struct.slots
-        _int32(parents, "parents", slots)
-        _int32(table_out, "table_out", slots, cache.struct.table_width)
-        _int32(held_out, "held_out", slots)
-        _int32(lens_out, "lens_out", slots)
-        _int32(status, "status", 1)
-        self._ok(lib.tb_kv_fork(self._h, cache.ref, parents.data_ptr(), table_out.data_ptr(),
-                                held_out.data_ptr(), lens_out.data_ptr(), status.data_ptr(),
-                                stream_handle(stream)), "tb_kv_fork")
+        slots = cache.per_slot
+        self._ok(lib.tb_kv_fork(self._h, cache.ref, _int32(parents, "parents", slots),
+                                _int32(table_out, "table_out", cache.table_shape),
+                                _int32(held_out, "held_out", slots),
+                                _int32(lens_out, "lens_out", slots),
+                                _int32(status, "status", (1,)), stream_handle(stream)),
+                 "tb_kv_fork")
 
     def kv_compact(self, cache: KvCache, start, keep, count, status, stream=None):
         """tb_kv_compact: token start[s] + keep[s, i] moves to start[s] + i."""
-        slots = cache.struct.slots
-        _int32(start, "start", slots)
-        _int32(keep, "keep", slots, None)
-        _int32(count, "count", slots)
-        _int32(status, "status", slots)
-        self._ok(lib.tb_kv_compact(self._h, cache.ref, start.data_ptr(), keep.data_ptr(),
-                                   keep.shape[1], count.data_ptr(), status.data_ptr(),
+        slots, width = cache.per_slot, keep.shape[-1]
+        self._ok(lib.tb_kv_compact(self._h, cache.ref, _int32(start, "start", slots),
+                                   _int32(keep, "keep", slots + (width,)), width,
+                                   _int32(count, "count", slots), _int32(status, "status", slots),
                                    stream_handle(stream)), "tb_kv_compact")
 
     def tree_attention_workspace(self, cache: KvCache, q_heads: int) -> int:
@@ -684,29 +687,28 @@ class Context:
         type, q_start int32 [seqs + 1], mask int32 [rows, words] (bits, see
         tree_mask), workspace uint8 of tree_attention_workspace bytes; lse
         float32 [rows, q_heads] when wanted; scale defaults to dim ** -0.5."""
-        s = cache.struct
-        for t, what in ((q, "q"), (out, "out")):
-            if not t.is_cuda or _dtype_name(t) != cache.name or t.dim() != 3 \
-                    or t.shape[2] != s.head_dim or (t.shape[2] > 1 and t.stride(2) != 1):
-                raise ValueError(f"{what} must be a [rows, heads, {s.head_dim}] CUDA tensor of the "
-                                 "cache's type with a dense last dimension")
         rows, heads, dim = q.shape
-        if out.shape != q.shape:
-            raise ValueError("q and out differ in shape")
-        seqs = _int32(q_start, "q_start", None).shape[0] - 1
-        _int32(mask, "mask", rows, None)
-        if seq_slots is not None:
-            _int32(seq_slots, "seq_slots", seqs)
+        if q.dtype != cache.dtype or out.dtype != cache.dtype or not q.is_cuda or not out.is_cuda \
+                or out.shape != q.shape or dim != cache.head_dim:
+            raise ValueError(f"q and out must be [rows, heads, {cache.head_dim}] CUDA tensors of the "
+                             "cache's type")
+        (q_row, q_head, q_dim), (o_row, o_head, o_dim) = q.stride(), out.stride()
+        if dim > 1 and (q_dim != 1 or o_dim != 1):
+            raise ValueError("the last dimension of q and out must be dense")
+        starts = _int32(q_start, "q_start", q_start.shape[:1])
+        seqs, words = q_start.shape[0] - 1, mask.shape[-1]
+        bits = _int32(mask, "mask", (rows, words))
+        slots = 0 if seq_slots is None else _int32(seq_slots, "seq_slots", (seqs,))
         if lse is not None and (_dtype_name(lse) != "float32" or not lse.is_cuda
-                                or not lse.is_contiguous() or tuple(lse.shape) != (rows, heads)):
+                                or not lse.is_contiguous() or lse.shape != (rows, heads)):
             raise ValueError("lse must be a contiguous float32 [rows, q_heads] CUDA tensor")
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         e = q.element_size()
-        t = Tree(ct.pointer(s), layer, seqs, addr(seq_slots), q_start.data_ptr(), rows, heads,
+        t = Tree(cache.ptr, layer, seqs, slots, starts, rows, heads,
                  dim ** -0.5 if scale is None else scale, q.data_ptr(), out.data_ptr(),
-                 q.stride(0) * e, q.stride(1) * e, out.stride(0) * e, out.stride(1) * e, addr(lse),
-                 mask.data_ptr(), mask.shape[1], workspace.data_ptr(),
+                 q_row * e, q_head * e, o_row * e, o_head * e,
+                 0 if lse is None else lse.data_ptr(), bits, words, workspace.data_ptr(),
                  workspace.numel() * workspace.element_size())
         self._ok(lib.tb_tree_attention(self._h, ct.byref(t), stream_handle(stream)),
                  "tb_tree_attention")
