@@ -111,34 +111,29 @@ __global__ void __launch_bounds__(kPageThreads)
     }
 }
 
-// Sum over the CTA before this thread, and the CTA's total; warp_sums: 33 ints.
-__device__ int scan_before(int v, int *warp_sums, int &total)
+// Sums over the CTA before this thread, and the CTA's totals, of two counts at
+// a time; sums: 32 words.
+__device__ int2 scan_before(int2 v, int2 *sums, int2 &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    int2 x = v;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d)
-            x += y;
+        const int a = __shfl_up_sync(0xffffffffu, x.x, d), b = __shfl_up_sync(0xffffffffu, x.y, d);
+        if (lane >= d) {
+            x.x += a;
+            x.y += b;
+        }
     }
     __syncthreads();
     if (lane == 31)
-        warp_sums[warp] = x;
+        sums[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int y = __shfl_up_sync(0xffffffffu, w, d);
-            if (lane >= d)
-                w += y;
-        }
-        warp_sums[lane] = w;
-    }
-    __syncthreads();
-    total = warp_sums[31];
-    return x - v + (warp ? warp_sums[warp - 1] : 0);
+    const int2 w = lane < (int)(blockDim.x >> 5) ? sums[lane] : int2{0, 0};
+    total = int2{__reduce_add_sync(0xffffffffu, w.x), __reduce_add_sync(0xffffffffu, w.y)};
+    const int2 before{__reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0),
+                      __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0)};
+    return int2{x.x - v.x + before.x, x.y - v.y + before.y};
 }
 
 __device__ __forceinline__ int pages_for(int tokens, int page_tokens)
@@ -189,92 +184,127 @@ __device__ __forceinline__ void store_remote(int *local, uint32_t rank, int valu
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(value) : "memory");
 }
 
+// 1024 pages of a warp's share: four bits for each 128 of them, the lane's
+// four pages; a set bit is a free page.
+constexpr int kGroupPages = 1024;
+constexpr int kHeldGroups = 4;  // groups kept in registers between the passes
+
+struct FreePages {
+    int from, to;                  // this warp's share
+    uint32_t group[kHeldGroups];   // its first groups
+};
+
 struct FreeCount {
     int cta[kCluster];      // free pages in each CTA's share
     int warp[kPlanWarps];   // ... in each warp's, this CTA
 };
 
-// This warp's share of the pages, in multiples of 128.
-__device__ __forceinline__ void page_share(const KvView &c, int &from, int &to)
+__device__ __forceinline__ uint32_t free_group(const KvView &c, int from, int to)
+{
+    const int lane = threadIdx.x & 31;
+    const bool wide = (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kGroupPages / 128; ++i) {
+        const int p = from + 128 * i + 4 * lane;
+        if (wide && p + 4 <= to) {
+            const int4 r = *reinterpret_cast<const int4 *>(c.refs + p);
+            bits |= (uint32_t)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << 4 * i;
+        } else {
+            for (int k = 0; k < 4; ++k)
+                if (p + k < to && c.refs[p + k] == 0)
+                    bits |= 1u << (4 * i + k);
+        }
+    }
+    return bits;
+}
+
+// The first look at this warp's share: its loads depend on nothing else.
+__device__ __forceinline__ void find_free(const KvView &c, FreePages &f)
 {
     const int shares = (int)cluster_size() * kPlanWarps;
     const int mine = (int)cluster_rank() * kPlanWarps + (int)(threadIdx.x >> 5);
     const int blocks = c.pages / 128 + (c.pages % 128 != 0);
     const int each = blocks / shares, more = blocks % shares;
     const int first = each * mine + min(mine, more), count = each + (mine < more);
-    from = min(first * 128, c.pages);  // pages <= 2^30
-    to = min(from + count * 128, c.pages);
+    f.from = min(first * 128, c.pages);  // pages <= 2^30
+    f.to = min(f.from + count * 128, c.pages);
+#pragma unroll
+    for (int g = 0; g < kHeldGroups; ++g)
+        f.group[g] = f.from + g * kGroupPages < f.to ? free_group(c, f.from + g * kGroupPages, f.to) : 0;
 }
 
-// Which of pages p .. p + 3 are free, as bits; one 16-byte load.
-__device__ __forceinline__ uint32_t free_bits(const KvView &c, int p, int to)
+// All threads of the cluster; orders their memory accesses before and after.
+template <bool CLUSTER>
+__device__ __forceinline__ void plan_sync()
 {
-    if (p + 4 <= to && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
-        const int4 r = *reinterpret_cast<const int4 *>(c.refs + p);
-        return (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
-    }
-    uint32_t bits = 0;
-    for (int k = 0; k < 4; ++k)
-        if (p + k < to && c.refs[p + k] == 0)
-            bits |= 1u << k;
-    return bits;
+    if (CLUSTER)
+        cluster_sync();
+    else
+        __syncthreads();
 }
 
 // Free pages of the pool; all threads of the cluster call it, after a
-// cluster_sync that says that every CTA runs.
-__device__ int count_free(const KvView &c, FreeCount &f)
+// plan_sync that says that every CTA runs.
+template <bool CLUSTER>
+__device__ int count_free(const KvView &c, const FreePages &pages, FreeCount &f)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int from, to, mine = 0;
-    page_share(c, from, to);
-#pragma unroll 4
-    for (int p = from + lane * 4; p < to; p += 128)
-        mine += __popc(free_bits(c, p, to));
+    int mine = 0;
+#pragma unroll
+    for (int g = 0; g < kHeldGroups; ++g)
+        mine += __popc(pages.group[g]);
+    for (int p = pages.from + kHeldGroups * kGroupPages; p < pages.to; p += kGroupPages)
+        mine += __popc(free_group(c, p, pages.to));
     mine = __reduce_add_sync(0xffffffffu, mine);
     if (lane == 0)
         f.warp[warp] = mine;
     __syncthreads();
-    if (warp == 0) {
-        const int sum = __reduce_add_sync(0xffffffffu, f.warp[lane]);
-        if (lane < (int)cluster_size())
-            store_remote(&f.cta[cluster_rank()], lane, sum);
-    }
+    const int sum = __reduce_add_sync(0xffffffffu, f.warp[lane]);
+    if (!CLUSTER)
+        return sum;
+    if (warp == 0 && lane < (int)cluster_size())
+        store_remote(&f.cta[cluster_rank()], lane, sum);
     cluster_sync();
-    int total = 0;
-    for (uint32_t r = 0; r < cluster_size(); ++r)
-        total += f.cta[r];
-    return total;
+    return __reduce_add_sync(0xffffffffu, lane < (int)cluster_size() ? f.cta[lane] : 0);
 }
 
 // Calls take(rank, page) for the `wanted` lowest free pages, after count_free.
-template <class Take>
-__device__ void take_free(const KvView &c, const FreeCount &f, int wanted, Take take)
+template <bool CLUSTER, class Take>
+__device__ void take_free(const KvView &c, const FreePages &pages, const FreeCount &f, int wanted,
+                          Take take)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int rank = 0, from, to;
-    for (uint32_t r = 0; r < cluster_rank(); ++r)
-        rank += f.cta[r];
-    for (int w = 0; w < warp; ++w)
-        rank += f.warp[w];
-    page_share(c, from, to);
-    const int end = rank + f.warp[warp];
-    for (int base = from; base < to && rank < wanted && rank < end; base += 128) {
-        const uint32_t bits = free_bits(c, base + lane * 4, to);
-        int before = __popc(bits);
-        for (int d = 1; d < 32; d *= 2) {
-            const int y = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= d)
-                before += y;
-        }
-        const int total = __shfl_sync(0xffffffffu, before, 31);
-        int mine = rank + before - __popc(bits);
-        for (int k = 0; k < 4; ++k)
-            if (bits >> k & 1) {
-                if (mine < wanted)
-                    take(mine, base + lane * 4 + k);
-                ++mine;
+    int rank = __reduce_add_sync(0xffffffffu, lane < warp ? f.warp[lane] : 0);
+    if (CLUSTER)
+        rank += __reduce_add_sync(0xffffffffu, lane < (int)cluster_rank() ? f.cta[lane] : 0);
+    const int end = min(rank + f.warp[warp], wanted);
+    for (int g = 0; rank < end; ++g) {
+        const int first = pages.from + g * kGroupPages;
+        uint32_t bits = 0;
+        if (g >= kHeldGroups)
+            bits = free_group(c, first, pages.to);
+#pragma unroll
+        for (int k = 0; k < kHeldGroups; ++k)
+            if (g == k)
+                bits = pages.group[k];
+        for (int i = 0; i < kGroupPages / 128; ++i) {
+            const uint32_t four = bits >> 4 * i & 15u;
+            int before = 0, total = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t have = __ballot_sync(0xffffffffu, four >> k & 1u);
+                before += __popc(have & ((1u << lane) - 1));
+                total += __popc(have);
             }
-        rank += total;
+            for (int k = 0, mine = rank + before; k < 4; ++k)
+                if (four >> k & 1u) {
+                    if (mine < wanted)
+                        take(mine, first + 128 * i + 4 * lane + k);
+                    ++mine;
+                }
+            rank += total;
+        }
     }
 }
 
@@ -292,6 +322,7 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
     return lo;
 }
 
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads)
     k_kv_resize(const KvView c, const int32_t *capacity, int32_t *status)
 {
@@ -299,14 +330,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     int *first_new = shared;              // [slots] pages that the slots before it take
     int *first_gone = shared + c.slots;   // [slots] ... give back
     int *held = shared + 2 * c.slots;     // [slots]
-    __shared__ int warp_sums[33];
+    __shared__ int2 warp_sums[32];
     __shared__ FreeCount found;
     __shared__ int bad;
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     if (threadIdx.x == 0)
         bad = 0;
-    cluster_sync();
+    FreePages pages;
+    find_free(c, pages);
+    plan_sync<CLUSTER>();
     int wanted = 0, gone = 0;
     for (int base = 0; base < c.slots; base += blockDim.x) {
         const int s = base + (int)threadIdx.x;
@@ -328,32 +361,31 @@ __global__ void __launch_bounds__(kPlanThreads)
                 shrink = max(has - need, 0);
             }
         }
-        int total;
-        const int before = scan_before(grow, warp_sums, total);
-        if (s < c.slots)
-            first_new[s] = wanted + before;
-        wanted += total;
-        const int before_gone = scan_before(shrink, warp_sums, total);
-        if (s < c.slots)
-            first_gone[s] = gone + before_gone;
-        gone += total;
+        int2 total;
+        const int2 before = scan_before(int2{grow, shrink}, warp_sums, total);
+        if (s < c.slots) {
+            first_new[s] = wanted + before.x;
+            first_gone[s] = gone + before.y;
+        }
+        wanted += total.x;
+        gone += total.y;
     }
     __syncthreads();
     int missing = 0;
     if (wanted)
-        missing = max(wanted - count_free(c, found), 0);
+        missing = max(wanted - count_free<CLUSTER>(c, pages, found), 0);
     const int verdict = bad ? -1 : missing;
     if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
     if (!verdict && wanted)
-        take_free(c, found, wanted, [&](int rank, int p) {
+        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int p) {
             const int s = last_at_most(first_new, c.slots, rank);
             c.table[(int64_t)s * c.width + held[s] + rank - first_new[s]] = p;
             c.refs[p] = 1;
         });
     // Pages are given back after every CTA has looked for free ones, and
     // nothing is written before all have read held and lens.
-    cluster_sync();
+    plan_sync<CLUSTER>();
     if (verdict)
         return;
     const int threads = (int)cluster_size() * kPlanThreads;
@@ -385,13 +417,14 @@ __global__ void __launch_bounds__(kPlanThreads)
 // those pages.  It enters the page that holds the part-filled one's tokens in
 // the output row of every slot that does not simply go on: the launch after it
 // copies where that is another page, and leaves the entry alone.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads)
     k_fork_plan(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *status)
 {
     extern __shared__ int shared[];
     int *heir = shared;               // [slots]: -1: the slot goes on; else its lowest child
     int *needy = shared + c.slots;    // slots that take a fresh page, in order
-    __shared__ int warp_sums[33];
+    __shared__ int2 warp_sums[32];
     __shared__ FreeCount found;
     __shared__ int bad;
     pdl_launch_dependents();
@@ -400,7 +433,9 @@ __global__ void __launch_bounds__(kPlanThreads)
         bad = 0;
     for (int s = threadIdx.x; s < c.slots; s += blockDim.x)
         heir[s] = INT32_MAX;
-    cluster_sync();
+    FreePages pages;
+    find_free(c, pages);
+    plan_sync<CLUSTER>();
     for (int s = threadIdx.x; s < c.slots; s += blockDim.x) {
         const int p = parents[s];
         if (p >= c.slots)
@@ -425,21 +460,21 @@ __global__ void __launch_bounds__(kPlanThreads)
                 }
             }
         }
-        int total;
-        const int before = scan_before(takes, warp_sums, total);
+        int2 total;
+        const int2 before = scan_before(int2{takes, 0}, warp_sums, total);
         if (takes)
-            needy[wanted + before] = s;
-        wanted += total;
+            needy[wanted + before.x] = s;
+        wanted += total.x;
     }
     __syncthreads();
     int missing = 0;
     if (wanted)
-        missing = max(wanted - count_free(c, found), 0);
+        missing = max(wanted - count_free<CLUSTER>(c, pages, found), 0);
     const int verdict = bad ? -1 : missing;
     if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
     if (!verdict && wanted)
-        take_free(c, found, wanted, [&](int rank, int page) {
+        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int page) {
             const int s = needy[rank], p = parents[s];
             table_out[(int64_t)s * c.width + c.lens[p] / c.page_tokens] = page;
             c.refs[page] = 1;
@@ -524,9 +559,9 @@ __global__ void __launch_bounds__(kPageThreads)
 // Compact
 // ---------------------------------------------------------------------------
 // A token's rows of one layer are split into 16-byte columns; a thread walks
-// one column through the slot's list.  It reads kAhead tokens, then writes
-// them: every later source lies past every destination written so far (keep
-// ascends, so keep[i] >= i), so no column needs another's progress.
+// one column through the slot's list, reading ahead of what it writes: every
+// later source lies past every destination written so far (keep ascends, so
+// keep[i] >= i), so no column needs another's progress.
 constexpr int kAhead = 16;
 constexpr int kCompactBlock = 128;   // list entries looked up at a time
 constexpr int kCompactThreads = 64;  // small CTAs: the columns spread over more SMs
@@ -599,16 +634,27 @@ __global__ void __launch_bounds__(kCompactThreads)
         __syncthreads();
         if (!base)
             continue;
-        for (int k = 0; k < here; k += kAhead) {
-            uint4 v[kAhead];
+        // Two sets of kAhead tokens: the next set is read before this one is
+        // written (its sources lie past this one's destinations).
+        uint4 v[2][kAhead];
+        auto read = [&](uint4(&x)[kAhead], int k) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (k + u < here)
-                    v[u] = *reinterpret_cast<const uint4 *>(base + from[k + u]);
+                    x[u] = *reinterpret_cast<const uint4 *>(base + from[k + u]);
+        };
+        auto write = [&](const uint4(&x)[kAhead], int k) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (k + u < here)
-                    *reinterpret_cast<uint4 *>(base + to[k + u]) = v[u];
+                    *reinterpret_cast<uint4 *>(base + to[k + u]) = x[u];
+        };
+        read(v[0], 0);
+        for (int k = 0; k < here; k += 2 * kAhead) {
+            read(v[1], k + kAhead);
+            write(v[0], k);
+            read(v[0], k + 2 * kAhead);
+            write(v[1], k + kAhead);
         }
     }
 }
@@ -650,21 +696,23 @@ cudaError_t launch_copy_pages(const KvView &c, const int32_t *src, const int32_t
 
 namespace {
 
-// Launches a kernel that hands out pages: its CTAs are one cluster.
+// Launches a kernel that hands out pages: its CTAs are one cluster, or one CTA.
 template <class... Args>
-cudaError_t launch_plan(void (*kernel)(Args...), const KvView &c, size_t smem, bool pdl,
+cudaError_t launch_plan(void (*many)(Args...), void (*one)(Args...), const KvView &c, size_t smem, bool pdl,
                         cudaStream_t stream, Args... args)
 {
-    const int cluster = c.pages > kClusterPages ? kCluster : 1;
+    const bool cluster = c.pages > kClusterPages;
+    void (*kernel)(Args...) = cluster ? many : one;
     cudaError_t e = cudaSuccess;
-    if (cluster > 8)
+    if (cluster)
         e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess && smem > 40 * 1024)  // beside the static shared memory
         e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem);
     if (e != cudaSuccess)
         return e;
-    return launch(kernel, dim3(cluster), kPlanThreads, smem, cluster, pdl, stream, args...);
+    const int ctas = cluster ? kCluster : 1;
+    return launch(kernel, dim3(ctas), kPlanThreads, smem, ctas, pdl, stream, args...);
 }
 
 }  // namespace
@@ -672,7 +720,7 @@ cudaError_t launch_plan(void (*kernel)(Args...), const KvView &c, size_t smem, b
 cudaError_t launch_kv_resize(const KvView &c, const int32_t *capacity, int32_t *status, bool pdl,
                              cudaStream_t stream)
 {
-    return launch_plan(k_kv_resize, c, 3 * c.slots * sizeof(int), pdl, stream, c, capacity, status);
+    return launch_plan(k_kv_resize<true>, k_kv_resize<false>, c, 3 * c.slots * sizeof(int), pdl, stream, c, capacity, status);
 }
 
 cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *table_out,
@@ -680,8 +728,8 @@ cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *tab
                            bool pdl, cudaStream_t stream)
 {
     (void)num_sms;
-    const cudaError_t e = launch_plan(k_fork_plan, c, 2 * c.slots * sizeof(int), pdl, stream, c, parents,
-                                      table_out, status);
+    const cudaError_t e = launch_plan(k_fork_plan<true>, k_fork_plan<false>, c, 2 * c.slots * sizeof(int),
+                                      pdl, stream, c, parents, table_out, status);
     if (e != cudaSuccess)
         return e;
     const int per_row = (c.width + kPageThreads - 1) / kPageThreads, rows = c.slots * per_row;
