@@ -184,8 +184,8 @@ __device__ __forceinline__ void store_remote(int *local, uint32_t rank, int valu
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(value) : "memory");
 }
 
-// 1024 pages of a warp's share: four bits for each 128 of them, the lane's
-// four pages; a set bit is a free page.
+// 1024 pages of a warp's share: a lane's word has the bits of 32 neighbouring
+// ones, a set bit is a free page.
 constexpr int kGroupPages = 1024;
 constexpr int kHeldGroups = 4;  // groups kept in registers between the passes
 
@@ -216,7 +216,15 @@ __device__ __forceinline__ uint32_t free_group(const KvView &c, int from, int to
                     bits |= 1u << (4 * i + k);
         }
     }
-    return bits;
+    // Read four pages a lane, 128 a step; wanted 32 a lane: step lane / 4, and
+    // eight lanes' four bits of it.
+    uint32_t word = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t other = __shfl_sync(0xffffffffu, bits, 8 * (lane & 3) + k);
+        word |= (other >> 4 * (lane >> 2) & 15u) << 4 * k;
+    }
+    return word;
 }
 
 // The first look at this warp's share: its loads depend on nothing else.
@@ -269,7 +277,8 @@ __device__ int count_free(const KvView &c, const FreePages &pages, FreeCount &f)
     return __reduce_add_sync(0xffffffffu, lane < (int)cluster_size() ? f.cta[lane] : 0);
 }
 
-// Calls take(rank, page) for the `wanted` lowest free pages, after count_free.
+// Hands out the `wanted` lowest free pages, after count_free: take(rank, n, bits,
+// page) gets the first n of the set bits of `bits`, pages page .. page + 31.
 template <bool CLUSTER, class Take>
 __device__ void take_free(const KvView &c, const FreePages &pages, const FreeCount &f, int wanted,
                           Take take)
@@ -288,23 +297,17 @@ __device__ void take_free(const KvView &c, const FreePages &pages, const FreeCou
         for (int k = 0; k < kHeldGroups; ++k)
             if (g == k)
                 bits = pages.group[k];
-        for (int i = 0; i < kGroupPages / 128; ++i) {
-            const uint32_t four = bits >> 4 * i & 15u;
-            int before = 0, total = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t have = __ballot_sync(0xffffffffu, four >> k & 1u);
-                before += __popc(have & ((1u << lane) - 1));
-                total += __popc(have);
-            }
-            for (int k = 0, mine = rank + before; k < 4; ++k)
-                if (four >> k & 1u) {
-                    if (mine < wanted)
-                        take(mine, first + 128 * i + 4 * lane + k);
-                    ++mine;
-                }
-            rank += total;
+        const int n = __popc(bits);
+        int before = n;
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d)
+                before += y;
         }
+        const int total = __shfl_sync(0xffffffffu, before, 31), mine = rank + before - n;
+        if (n && mine < end)
+            take(mine, min(n, end - mine), bits, first + 32 * lane);
+        rank += total;
     }
 }
 
@@ -323,7 +326,7 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
 }
 
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     k_kv_resize(const KvView c, const int32_t *capacity, int32_t *status)
 {
     extern __shared__ int shared[];
@@ -378,10 +381,15 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
     if (!verdict && wanted)
-        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int p) {
-            const int s = last_at_most(first_new, c.slots, rank);
-            c.table[(int64_t)s * c.width + held[s] + rank - first_new[s]] = p;
-            c.refs[p] = 1;
+        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int n, uint32_t bits, int page) {
+            int s = last_at_most(first_new, c.slots, rank);
+            for (; n; --n, ++rank, bits &= bits - 1) {
+                while (s + 1 < c.slots && first_new[s + 1] <= rank)
+                    ++s;
+                const int p = page + __ffs(bits) - 1;
+                c.table[(int64_t)s * c.width + held[s] + rank - first_new[s]] = p;
+                c.refs[p] = 1;
+            }
         });
     // Pages are given back after every CTA has looked for free ones, and
     // nothing is written before all have read held and lens.
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 // the output row of every slot that does not simply go on: the launch after it
 // copies where that is another page, and leaves the entry alone.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     k_fork_plan(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *status)
 {
     extern __shared__ int shared[];
@@ -474,10 +482,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (cluster_rank() == 0 && threadIdx.x == 0)
         *status = verdict;
     if (!verdict && wanted)
-        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int page) {
-            const int s = needy[rank], p = parents[s];
-            table_out[(int64_t)s * c.width + c.lens[p] / c.page_tokens] = page;
-            c.refs[page] = 1;
+        take_free<CLUSTER>(c, pages, found, wanted, [&](int rank, int n, uint32_t bits, int page) {
+            for (; n; --n, ++rank, bits &= bits - 1) {
+                const int s = needy[rank], p = page + __ffs(bits) - 1;
+                table_out[(int64_t)s * c.width + c.lens[parents[s]] / c.page_tokens] = p;
+                c.refs[p] = 1;
+            }
         });
 }
 
