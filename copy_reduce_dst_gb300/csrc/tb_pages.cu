@@ -566,32 +566,20 @@ __global__ void __launch_bounds__(kPageThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Compact
+// Compact.  A token's rows of one layer are split into 16-byte columns; a
+// thread walks one column through the slot's list, reading ahead of what it
+// writes: every later source lies past every destination written so far (keep
+// ascends, so keep[i] >= i), so no column needs another's progress.  A CTA is
+// one warp: the columns of a few slots still spread over all SMs.
 // ---------------------------------------------------------------------------
-// A token's rows of one layer are split into 16-byte columns; a thread walks
-// one column through the slot's list, reading ahead of what it writes: every
-// later source lies past every destination written so far (keep ascends, so
-// keep[i] >= i), so no column needs another's progress.
-constexpr int kAhead = 16;
-constexpr int kCompactBlock = 128;   // list entries looked up at a time
-constexpr int kCompactThreads = 64;  // small CTAs: the columns spread over more SMs
 
-__global__ void __launch_bounds__(kCompactThreads)
-    k_kv_compact(const KvView c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
-                 const int32_t *count, int32_t *status)
+// Whether slot s's list may be carried out, as tb_kv_compact's status; the
+// whole CTA calls it.
+__device__ int compact_verdict(const KvView &c, int s, int64_t first, const int32_t *list, int n, int most)
 {
     __shared__ int verdict, skip;
-    __shared__ int64_t from[kCompactBlock], to[kCompactBlock];
-    pdl_launch_dependents();
-    pdl_wait_prerequisite();
-    const int s = blockIdx.y, n = count[s], P = c.page_tokens;
-    const int64_t first = start[s];
-    const int32_t *list = keep + (int64_t)s * keep_stride, *row = c.table + (int64_t)s * c.width;
-    if (n < 0) {
-        if (blockIdx.x == 0 && threadIdx.x == 0)
-            status[s] = 0;
-        return;
-    }
+    const int P = c.page_tokens;
+    const int32_t *row = c.table + (int64_t)s * c.width;
     if (threadIdx.x == 0) {
         verdict = 0;
         skip = n;
@@ -599,7 +587,7 @@ __global__ void __launch_bounds__(kCompactThreads)
     __syncthreads();
     const int held = min(max(c.held[s], 0), c.width);
     const int64_t room = (int64_t)held * P;
-    if (n > keep_stride || first < 0 || first + n > room)
+    if (n > most || first < 0 || first + n > room)
         verdict = 2;
     else
 #pragma unroll 4
@@ -612,61 +600,142 @@ __global__ void __launch_bounds__(kCompactThreads)
                 atomicMin(&skip, i);  // tokens before the first that moves stay where they are
         }
     __syncthreads();
-    if (verdict == 0) {
+    const bool bad = verdict != 0;
+    __syncthreads();
+    if (!bad) {
         // From the first page written, or the page of the new end, on: none shared.
         for (int64_t j = (first + skip) / P + threadIdx.x; j < held; j += blockDim.x)
             if (is_page(c, row[j]) && c.refs[row[j]] > 1)
                 verdict = 1;
     }
     __syncthreads();
-    if (blockIdx.x == 0 && threadIdx.x == 0)
+    return verdict;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1)
+    k_compact_check(const KvView c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
+                    const int32_t *count, int32_t *status)
+{
+    pdl_launch_dependents();
+    pdl_wait_prerequisite();
+    const int s = blockIdx.x, n = count[s];
+    const int verdict =
+        n < 0 ? 0 : compact_verdict(c, s, start[s], keep + (int64_t)s * keep_stride, n, keep_stride);
+    if (threadIdx.x == 0) {
         status[s] = verdict;
-    if (verdict)
+        if (n >= 0 && !verdict)
+            c.lens[s] = start[s] + n;
+    }
+}
+
+constexpr int kSet = 8;         // tokens requested at a time
+constexpr int kRing = 8;        // sets on their way to shared memory, where only their thread reads them
+constexpr int kLookAhead = 4;   // blocks of 32 list entries looked up, or in use
+constexpr int kFusedList = 256; // longest list that the moving CTAs check themselves
+
+// CHECK: no k_compact_check has run.
+template <bool CHECK>
+__global__ void __launch_bounds__(32)
+    k_kv_compact(const KvView c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
+                 const int32_t *count, int32_t *status)
+{
+    __shared__ __align__(16) uint4 ring[kRing][kSet][32];
+    __shared__ __align__(16) int64_t from[kLookAhead][32], to[kLookAhead][32];
+    pdl_launch_dependents();
+    pdl_wait_prerequisite();
+    const int s = blockIdx.y, n = count[s], P = c.page_tokens, lane = threadIdx.x;
+    const int64_t first = start[s];
+    const int32_t *list = keep + (int64_t)s * keep_stride, *row = c.table + (int64_t)s * c.width;
+    if (CHECK) {
+        const int verdict = n < 0 ? 0 : compact_verdict(c, s, first, list, n, keep_stride);
+        if (blockIdx.x == 0 && lane == 0) {
+            status[s] = verdict;
+            if (n >= 0 && !verdict)
+                c.lens[s] = (int32_t)(first + n);
+        }
+        if (verdict)
+            return;
+    } else if (status[s]) {
         return;
-    if (blockIdx.x == 0 && threadIdx.x == 0)
-        c.lens[s] = (int32_t)(first + n);
+    }
+    if (n <= 0)
+        return;
     const uint32_t cols = c.row_bytes / 16;
-    const int64_t col = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t total = 2ll * c.layers * c.heads * cols;
+    const int64_t col = (int64_t)blockIdx.x * 32 + lane;
+    const bool real = col < 2ll * c.layers * c.heads * cols;
     char *base = nullptr;
-    if (col < total) {
-        const int64_t lane = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
-        base = pool_of(c, (int32_t)lane) + in / cols * c.head_stride + in % cols * 16;
+    if (real) {
+        const int64_t half = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
+        base = pool_of(c, (int32_t)half) + in / cols * c.head_stride + in % cols * 16;
     }
-    for (int b = skip; b < n; b += kCompactBlock) {
-        const int here = min(n - b, kCompactBlock);
-        __syncthreads();
-        for (int k = threadIdx.x; k < here; k += kCompactThreads) {
-            const int64_t f = first + list[b + k], t = first + b + k;
-            from[k] = row[f / P] * c.page_stride + f % P * c.token_stride;
-            to[k] = row[t / P] * c.page_stride + t % P * c.token_stride;
-        }
-        __syncthreads();
-        if (!base)
-            continue;
-        // Two sets of kAhead tokens: the next set is read before this one is
-        // written (its sources lie past this one's destinations).
-        uint4 v[2][kAhead];
-        auto read = [&](uint4(&x)[kAhead], int k) {
+    // Looking up a block of 32 entries takes two dependent loads; both are
+    // under way long before the block's tokens are requested.
+    auto entry = [&](int block) {
+        const int i = 32 * block + lane;
+        return i < n ? list[i] : 0;
+    };
+    auto pages = [&](int block, int k) {
+        const int i = 32 * block + lane;
+        return i < n ? int2{row[(first + k) / P], row[(first + i) / P]} : int2{0, 0};
+    };
+    auto keep_block = [&](int block, int k, int2 page) {
+        const int64_t f = first + k, t = first + 32 * block + lane;
+        const bool moves = 32 * block + lane < n && f != t;
+        from[block % kLookAhead][lane] = moves ? page.x * c.page_stride + f % P * c.token_stride : -1;
+        to[block % kLookAhead][lane] = moves ? page.y * c.page_stride + t % P * c.token_stride : -1;
+    };
+    auto places = [&](const int64_t(&of)[kLookAhead][32], int set, int64_t(&x)[kSet]) {
+        const int4 *p = reinterpret_cast<const int4 *>(&of[set / 4 % kLookAhead][set % 4 * kSet]);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (k + u < here)
-                    x[u] = *reinterpret_cast<const uint4 *>(base + from[k + u]);
-        };
-        auto write = [&](const uint4(&x)[kAhead], int k) {
+        for (int u = 0; u < kSet / 2; ++u)
+            reinterpret_cast<int4 *>(x)[u] = p[u];
+    };
+    auto request = [&](int set) {
+        int64_t f[kSet];
+        places(from, set, f);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (k + u < here)
-                    *reinterpret_cast<uint4 *>(base + to[k + u]) = x[u];
-        };
-        read(v[0], 0);
-        for (int k = 0; k < here; k += 2 * kAhead) {
-            read(v[1], k + kAhead);
-            write(v[0], k);
-            read(v[0], k + 2 * kAhead);
-            write(v[1], k + kAhead);
-        }
+        for (int u = 0; u < kSet; ++u)
+            if (f[u] >= 0 && real)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 smem_u32(&ring[set % kRing][u][lane])),
+                             "l"(base + f[u])
+                             : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int b = 0; b < 2; ++b) {
+        const int k = entry(b);
+        keep_block(b, k, pages(b, k));
     }
+    int k2 = entry(2), k3 = entry(3);
+    int2 p2 = pages(2, k2);
+    __syncwarp();
+    for (int k = 0; k < kRing - 1; ++k)
+        request(k);
+    const int sets = (n + kSet - 1) / kSet;
+    for (int k = 0; k < sets; ++k) {
+        if (k % 4 == 0) {  // a block of four sets begins; requests reach into the second after it
+            const int block = k / 4;
+            keep_block(block + 2, k2, p2);
+            k2 = k3;
+            p2 = pages(block + 3, k2);
+            k3 = entry(block + 4);
+            __syncwarp();
+        }
+        request(k + kRing - 1);
+        int64_t d[kSet];
+        uint4 v[kSet];
+        places(to, k, d);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+#pragma unroll
+        for (int u = 0; u < kSet; ++u)
+            v[u] = ring[k % kRing][u][lane];
+#pragma unroll
+        for (int u = 0; u < kSet; ++u)
+            if (d[u] >= 0 && real)
+                *reinterpret_cast<uint4 *>(base + d[u]) = v[u];
+        __syncwarp();
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -753,8 +822,16 @@ cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32
                               bool pdl, cudaStream_t stream)
 {
     const int64_t cols = 2ll * c.layers * c.heads * (c.row_bytes / 16);
-    return launch(k_kv_compact, dim3((unsigned)((cols + kCompactThreads - 1) / kCompactThreads), c.slots),
-                  kCompactThreads, 0, 1, pdl, stream, c, start, keep, keep_stride, count, status);
+    const dim3 grid((unsigned)((cols + 31) / 32), c.slots);
+    if (keep_stride <= kFusedList)
+        return launch(k_kv_compact<true>, grid, 32, 0, 1, pdl, stream, c, start, keep, keep_stride, count,
+                      status);
+    const cudaError_t e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start,
+                                 keep, keep_stride, count, status);
+    if (e != cudaSuccess)
+        return e;
+    return launch(k_kv_compact<false>, grid, 32, 0, 1, pdl, stream, c, start, keep, keep_stride, count,
+                  status);
 }
 
 }  // namespace tb
