@@ -252,6 +252,13 @@ int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream)
         return fail(ctx, TB_ENOTSUP, "tree_attention: more than %d sequences", TB_TREE_MAX_SEQS);
     if (t->rows > (1 << 29) || t->rows > INT_MAX / t->q_heads)
         return fail(ctx, TB_ENOTSUP, "tree_attention: rows exceeds 2^29 or rows * q_heads 2^31 - 1");
+    // Work is counted in 32 bits, in tiles of 128 positions: what the longest
+    // rows of the table and all query rows could make of it.
+    const int64_t tiles = (int64_t)c.table_width * c.page_tokens / 128 + t->rows / 128 + 8;
+    const int64_t units = (int64_t)t->rows * (t->q_heads / c.kv_heads) / 128 + t->seqs;
+    if (units * c.kv_heads > INT_MAX / tiles)
+        return fail(ctx, TB_ENOTSUP, "tree_attention: rows, heads and table_width make more than 2^31 - 1 "
+                                     "tiles of work");
     if (!t->seq_slots && t->seqs > c.slots)
         return fail(ctx, TB_EINVAL, "tree_attention: more sequences than slots");
     if (!isfinite(t->scale))

@@ -58,88 +58,99 @@ __device__ __forceinline__ Seq seq_of(const TreePlan &p, int b, int unit_rows)
     return s;
 }
 
-__device__ __forceinline__ int64_t seq_work(const TreePlan &p, int b, int unit_rows)
+// Work is counted in 32 bits; the host refuses calls that might have more.
+__device__ __forceinline__ int work_of(const TreePlan &p, const Seq &s)
 {
-    const Seq s = seq_of(p, b, unit_rows);
-    return (int64_t)s.units * p.c.heads * (s.tiles + kUnitCost);
-}
-
-// a / b for 0 <= a, 0 < b; 64-bit divisions cost hundreds of cycles.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
-{
-    return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+    return s.units * p.c.heads * (s.tiles + kUnitCost);
 }
 
 struct Place {
-    int64_t total;  // work of all units
-    int64_t at;     // where the run begins
-    int64_t off;    // ... counted from the beginning of its sequence
+    int total;  // work of all units
+    int at;     // where the run begins
+    int off;    // ... counted from the beginning of its sequence
     int b;
-    int ctas;       // CTAs that get a run
-    int64_t each;   // work of every run; `more` of the runs have one on top
-    uint32_t more;
+    int ctas;   // CTAs that get a run
+    int each;   // work of every run; `more` of the runs have one on top
+    int more;
+    Seq s;
     // Start of run c.
-    __device__ int64_t start(int c) const { return each * c + more * (uint32_t)c / (uint32_t)ctas; }
+    __device__ int start(int c) const { return each * c + (int)((uint32_t)(more * c) / (uint32_t)ctas); }
+};
+
+// Shared memory of find_run.
+struct Found {
+    int sum[32], b, off;
+    Seq s;
 };
 
 // Where run `c` of at most `grid` runs begins; the whole block calls it.
-// words: 34 64-bit words of shared memory.
 template <int THREADS>
-__device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, int64_t *words)
+__device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Found &found)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto scan = [&](int64_t v, int64_t &sum) {  // sum before this thread; sum of all
-        int64_t x = v;
+    auto scan = [&](int v, int &sum) {  // sum before this thread; sum of all
+        int x = v;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d)
                 x += y;
         }
         __syncthreads();
         if (lane == 31)
-            words[warp] = x;
+            found.sum[warp] = x;
         __syncthreads();
-        int64_t before = x - v;
-        sum = 0;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            const int64_t y = words[w];
-            before += w < warp ? y : 0;
-            sum += y;
-        }
-        return before;
+        const int w = lane < THREADS / 32 ? found.sum[lane] : 0;
+        sum = __reduce_add_sync(0xffffffffu, w);
+        return x - v + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
     };
-    Place r;
-    int64_t mine = 0, one = 0;
-    for (int b = threadIdx.x; b < p.seqs; b += THREADS)
-        mine += one = seq_work(p, b, unit_rows);
-    int64_t before = scan(mine, r.total);
-    r.ctas = (int)(r.total < grid ? r.total : grid);
-    r.b = 0;
-    r.off = r.at = 0;
+    Place r{};
+    Seq s{};
+    int mine = 0, one = 0, count = 0;
+    for (int b = threadIdx.x; b < p.seqs; b += THREADS) {
+        s = seq_of(p, b, unit_rows);
+        mine += one = work_of(p, s);
+        count += s.units * p.c.heads;
+    }
+    int before = scan(mine, r.total);
+    r.ctas = min(r.total, grid);
+    if (unit_rows > kRowTile) {
+        // Units of one sequence and head read the same keys and values.  Where
+        // nearly as many runs as there are SMs make whole numbers of runs a
+        // unit (of equal ones), those units read a tile at the same time, and
+        // one of them finds it in L2.
+        int units;
+        scan(count, units);
+        if (units <= grid && grid / units * units >= grid - grid / 16)
+            r.ctas = min(r.total, grid / units * units);
+    }
     if (c >= r.ctas)
         return r;
-    r.each = divide(r.total, r.ctas);
-    r.more = (uint32_t)(r.total - r.each * r.ctas);
+    r.each = r.total / r.ctas;
+    r.more = r.total - r.each * r.ctas;
     r.at = r.start(c);
-    int64_t base = 0, sum = r.total;
+    int base = 0, sum = r.total;
     for (int first = 0; first < p.seqs; first += THREADS) {
         const int b = first + (int)threadIdx.x;
         if (p.seqs > THREADS) {
-            one = b < p.seqs ? seq_work(p, b, unit_rows) : 0;
-            before = scan(one, sum);
-        } else if (b >= p.seqs) {
             one = 0;
+            if (b < p.seqs) {
+                s = seq_of(p, b, unit_rows);
+                one = work_of(p, s);
+            }
+            before = scan(one, sum);
         }
-        if (r.at >= base + before && r.at < base + before + one) {
-            words[32] = b;
-            words[33] = r.at - base - before;
+        if (r.at >= base + before && r.at - base - before < one) {
+            found.b = b;
+            found.off = r.at - base - before;
+            found.s = s;
         }
         base += sum;
     }
     __syncthreads();
-    r.b = (int)words[32];
-    r.off = words[33];
+    r.b = found.b;
+    r.off = found.off;
+    r.s = found.s;
     return r;
 }
 
@@ -157,17 +168,13 @@ struct Unit {
 
 struct Walk {
     const TreePlan &p;
-    int64_t left;
-    int unit_rows, number, b, unit, at;  // unit: of the sequence, head by head; at: within its work
+    int left, unit_rows, number, b, unit, at;  // unit: of the sequence, head by head; at: within its work
     Seq s;
-    __device__ Walk(const TreePlan &plan, int rows, const Place &place, int64_t work)
-        : p(plan), left(work), unit_rows(rows), number(0), b(place.b)
+    __device__ Walk(const TreePlan &plan, int rows, const Place &place, int work)
+        : p(plan), left(work), unit_rows(rows), number(0), b(place.b), s(place.s)
     {
-        if (left > 0) {
-            s = seq_of(p, b, unit_rows);
-            unit = (int)divide(place.off, s.tiles + kUnitCost);
-            at = (int)(place.off - (int64_t)unit * (s.tiles + kUnitCost));
-        }
+        unit = place.off / (s.tiles + kUnitCost);
+        at = place.off - unit * (s.tiles + kUnitCost);
     }
     __device__ bool next(Unit &u)
     {
@@ -177,7 +184,7 @@ struct Walk {
                 unit = 0;
                 continue;
             }
-            const int end = (int)min((int64_t)s.tiles + kUnitCost, at + left);
+            const int end = min(s.tiles + kUnitCost, at + left);
             u.j0 = max(at - kUnitCost, 0);
             u.j1 = end - kUnitCost;
             left -= end - at;
@@ -226,7 +233,7 @@ struct Shape {
 // Barriers, by number (8 bytes each).
 enum {
     kFull = 0,        // [stage] has landed
-    kEmpty = 8,       // [stage] its readers are done
+    kEmpty = 8,       // [stage] its readers are done (a softmax warp says so)
     kTail = 16,       // [stage] values to be looked over have landed
     kQuery = 24,      // [stream] the query tile is in shared memory
     kScores = 26,     // [stream] scores are in tensor memory
@@ -238,7 +245,7 @@ enum {
 struct Misc {
     uint32_t tmem, abort;
     int bad[8];       // by unit: its number + 1 where a drafted value is not finite
-    int64_t words[34];
+    Found found;
 };
 static_assert(sizeof(Misc) <= 512, "Misc");
 
@@ -254,19 +261,25 @@ struct Cta {
         volatile uint32_t *abort = &misc->abort;
         if (limit ? mbar_try_wait(bar(i), parity) : mbar_test_wait(bar(i), parity))
             return true;
-        const uint64_t t0 = limit ? global_ns() : 0;
+        const uint64_t begun = limit ? global_ns() : 0;
         while (limit) {
             if (mbar_try_wait(bar(i), parity))
                 return true;
             if (*abort)
                 return false;
-            if (global_ns() - t0 > limit)
+            if (global_ns() - begun > limit)
                 break;
         }
         *abort = 1;
         if (status)
             *reinterpret_cast<volatile uint32_t *>(status) = 1u;
         return false;
+    }
+    // The same for a whole warp; all lanes ask, which measured faster than one
+    // asking for all (the large tree 258 us against 309).
+    __device__ bool wait_warp(int i, uint32_t parity) const
+    {
+        return __all_sync(0xffffffffu, wait(i, parity));
     }
 };
 
@@ -397,7 +410,7 @@ __device__ void fix_role(const TreePlan &p, const Cta &cta, Walk walk)
             for (int part = 0; part < S::kParts; ++part) {
                 const uint32_t item = k + (2 * (j - u.j0) + 1) * S::kParts + part;
                 const uint32_t stage = item % S::kStages, at = cta.smem + S::kRing + stage * S::kStage;
-                if (!__all_sync(0xffffffffu, cta.wait(kTail + stage, parity >> stage & 1)))
+                if (!cta.wait_warp(kTail + stage, parity >> stage & 1))
                     return;
                 parity ^= 1u << stage;
                 const int base = j * kTile + part * S::kPos;
@@ -533,47 +546,58 @@ __device__ void product_role(const TreePlan &p, const Cta &cta, Walk walk)
     constexpr uint32_t kScoreDesc = umma_idesc(S::BF16, S::kPos, false);
     constexpr uint32_t kSumDesc = umma_idesc(S::BF16, S::DP, true);
     const uint32_t tmem = cta.misc->tmem, ring = cta.smem + S::kRing;
-    uint32_t k = 0;                      // stages taken
+    uint32_t stage = 0, landed = 0;      // the next stage and the parity of its phase
     uint32_t weights[2] = {0, 0};        // weight tiles taken per stream
     uint32_t queries[2] = {0, 0};        // query tiles
     Unit u;
 
-    auto scores = [&](int stream, uint32_t stage, int part) {
-        const uint32_t q = cta.smem + stream * S::kQuery, key = ring + stage * S::kStage;
+    auto scores = [&](int stream, int part, uint32_t at) {
+        const uint32_t q = umma_desc_low(cta.smem + stream * S::kQuery, 0);
+        const uint32_t key = umma_desc_low(ring + at * S::kStage, 0);
+        const uint32_t d = tmem + S::score_col(stream) + part * S::kPos;
 #pragma unroll
         for (int kk = 0; kk < S::DP / 16; ++kk)
-            umma_ss(tmem + S::score_col(stream) + part * S::kPos,
-                    umma_desc(q + (kk >> 2) * (kRowTile * 128) + (kk & 3) * 32, 0),
-                    umma_desc(key + (kk >> 2) * S::kHalf + (kk & 3) * 32, 0), kScoreDesc, kk > 0);
+            umma_ss(d, umma_desc(q, (kk >> 2) * (kRowTile * 128) + (kk & 3) * 32),
+                    umma_desc(key, (kk >> 2) * S::kHalf + (kk & 3) * 32), kScoreDesc, kk > 0);
     };
-    auto sums = [&](int stream, uint32_t stage, int part, bool add) {
-        const uint32_t value = ring + stage * S::kStage;
+    auto sums = [&](int stream, int part, uint32_t at, bool add) {
+        const uint32_t value = umma_desc_low(ring + at * S::kStage, S::kHalf);
+        const uint32_t from = tmem + S::score_col(stream) + part * (S::kPos / 2);
+        const uint32_t d = tmem + S::sum_col(stream);
 #pragma unroll
         for (int kk = 0; kk < S::kPos / 16; ++kk)
-            umma_ts(tmem + S::sum_col(stream),
-                    tmem + S::score_col(stream) + part * (S::kPos / 2) + kk * 8,
-                    umma_desc(value + kk * 16 * 128, S::kHalf), kSumDesc, add || kk > 0);
+            umma_ts(d, from + kk * 8, umma_desc(value, kk * 16 * 128), kSumDesc, kk > 0 || add);
     };
-    auto landed = [&](uint32_t item) { return cta.wait(kFull + item % S::kStages, item / S::kStages & 1); };
+    // Waits for the next stage to land and takes it.
+    auto take = [&](uint32_t &at) {
+        at = stage;
+        if (!cta.wait(kFull + at, landed))
+            return false;
+        if (++stage == S::kStages) {
+            stage = 0;
+            landed ^= 1;
+        }
+        return true;
+    };
 
     while (walk.next(u)) {
         const int streams = u.rows > kRowTile ? 2 : 1;
         for (int j = u.j0; j <= u.j1; ++j) {
-            // Sums of tile j - 1 and scores of tile j, stream by stream.  Its
-            // stages: values k .. k + kParts - 1, then the keys.
-            const uint32_t keys = j > u.j0 ? k + S::kParts : k;
+            // Sums of tile j - 1 and scores of tile j, stream by stream.
+            uint32_t values[S::kParts], keys[S::kParts];
+#pragma unroll 1
             for (int s = 0; s < streams; ++s) {
-                const bool last = s + 1 == streams;
                 if (j > u.j0) {
                     if (!cta.wait(kWeights + s, weights[s]++ & 1))
                         return;
+#pragma unroll
                     for (int part = 0; part < S::kParts; ++part) {
-                        if (!landed(k + part))
+                        if (s == 0 && !take(values[part]))
                             return;
                         tc_fence_after();
-                        sums(s, (k + part) % S::kStages, part, j > u.j0 + 1 || part > 0);
-                        if (last)
-                            umma_commit(cta.bar(kEmpty + (k + part) % S::kStages));
+                        sums(s, part, values[part], j > u.j0 + 1 || part > 0);
+                        if (S::STREAMS == 1)
+                            umma_commit(cta.bar(kEmpty + values[part]));
                     }
                 } else if (!cta.wait(kQuery + s, queries[s]++ & 1)) {
                     return;
@@ -582,17 +606,17 @@ __device__ void product_role(const TreePlan &p, const Cta &cta, Walk walk)
                     umma_commit(cta.bar(kSums + s));
                     continue;
                 }
+#pragma unroll
                 for (int part = 0; part < S::kParts; ++part) {
-                    if (!landed(keys + part))
+                    if (s == 0 && !take(keys[part]))
                         return;
                     tc_fence_after();
-                    scores(s, (keys + part) % S::kStages, part);
-                    if (last)
-                        umma_commit(cta.bar(kEmpty + (keys + part) % S::kStages));
+                    scores(s, part, keys[part]);
+                    if (S::STREAMS == 1)
+                        umma_commit(cta.bar(kEmpty + keys[part]));
                 }
                 umma_commit(cta.bar(kScores + s));
             }
-            k = j == u.j1 ? keys : keys + S::kParts;
         }
     }
 }
@@ -632,9 +656,9 @@ __device__ void note_cut(const TreePlan &p, const Place &place, Walk walk)
     Cut cut{};
     Unit u;
     if ((int)blockIdx.x < place.ctas && walk.next(u) && u.j0 > 0) {
-        const int64_t begin = place.at - u.j0, end = begin + u.s.tiles;  // of its tiles
-        if (place.start(blockIdx.x - 1) <= begin) {
-            int last = (int)min(divide(end * place.ctas, place.total), (int64_t)place.ctas - 1);
+        const int begin = place.at - u.j0, end = begin + u.s.tiles;  // of its tiles
+        if (place.start((int)blockIdx.x - 1) <= begin) {
+            int last = (int)min((int64_t)end * place.ctas / place.total, (int64_t)place.ctas - 1);
             while (place.start(last) >= end)
                 --last;
             while (last + 1 < place.ctas && place.start(last + 1) < end)
@@ -773,10 +797,22 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
     Unit before, u;
     bool begun = false;
     float top = 0.0f, sum = 0.0f;
+    // Two CTAs on an SM have short rings: the issuing thread commits to the
+    // barrier of each stage.  With two streams the ring is longer, and the first
+    // thread of the unit's last stream hands the stages back when it hears of
+    // the products' end, which spares the issuing thread 100 cycles a commit.
+    uint32_t stage = 0;
+    auto hand_back = [&](const Unit &of) {
+        if (S::STREAMS == 1)
+            return;
+        if (stream * kRowTile + kRowTile >= of.rows && (threadIdx.x & 127) == 0)
+            mbar_arrive(cta.bar(kEmpty + stage));
+        stage = (stage + 1) % S::kStages;
+    };
     for (;;) {
         bool more;  // a further unit has rows for this stream
         while ((more = walk.next(u)) && u.rows <= stream * kRowTile)
-            ;
+            stage = (stage + 2 * u.tiles()) % S::kStages;
         // The query rows of the stream's tile are on their way while the last
         // unit's last product runs, and its first scores while the last sums
         // are read: those are not written again before this stream's next
@@ -802,9 +838,10 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             }
         }
         if (begun) {
-            if (!__all_sync(0xffffffffu, cta.wait(kSums + stream, sums_seen++ & 1)))
+            if (!cta.wait_warp(kSums + stream, sums_seen++ & 1))
                 return;
             tc_fence_after();
+            hand_back(before);  // the last values
         }
         if (more) {
 #pragma unroll
@@ -830,43 +867,41 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
         top = -INFINITY;
         sum = 0.0f;
         for (int j = u.j0; j < u.j1; ++j) {
-            if (!__all_sync(0xffffffffu, cta.wait(kScores + stream, tiles_seen++ & 1)))
+            if (!cta.wait_warp(kScores + stream, tiles_seen++ & 1))
                 return;
             tc_fence_after();
+            if (j > u.j0)
+                hand_back(u);  // the values of the tile before
+            hand_back(u);      // this tile's keys
             if (active) {
-                uint32_t s[2][32];
+                // Scores are read twice, 32 columns at a time: for the maximum,
+                // and for the weights, which take the place of scores already
+                // read.  (A read takes 20 cycles; holding all 128 in registers
+                // or unrolling this leaves too few of them for two CTAs, and
+                // code too long for the instruction cache.)
+                uint32_t s[32];
                 if (u.tail(j))  // what is hidden becomes -inf in its place
 #pragma unroll 1
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t seen = mask.seen(j * kTile + 32 * g - u.s.n);
                         if (__all_sync(0xffffffffu, seen == 0xffffffffu))
                             continue;
-                        tmem_load32(s[0], score_cols + 32 * g);
-                        tmem_wait_load(s[0]);
+                        tmem_load32(s, score_cols + 32 * g);
+                        tmem_wait_load(s);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            s[0][i] = seen >> i & 1 ? s[0][i] : 0xff800000u;
-                        tmem_store32(score_cols + 32 * g, s[0]);
+                            s[i] = seen >> i & 1 ? s[i] : 0xff800000u;
+                        tmem_store32(score_cols + 32 * g, s);
                         tmem_wait_store();
                     }
-                // Scores are read twice, 32 columns at a time with the next 32
-                // on their way: once for the maximum and once for the weights,
-                // which take the place of scores already read.  Holding all
-                // 128 instead leaves too few registers for two CTAs.
                 float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tmem_load32(s[0], score_cols);
 #pragma unroll 1
-                for (int g = 0; g < 4; g += 2) {
-                    tmem_wait_load(s[0]);
-                    tmem_load32(s[1], score_cols + 32 * (g + 1));
+                for (int g = 0; g < 4; ++g) {
+                    tmem_load32(s, score_cols + 32 * g);
+                    tmem_wait_load(s);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[0][i]));
-                    tmem_wait_load(s[1]);
-                    tmem_load32(s[0], score_cols + 32 * (g + 2 & 3));
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[1][i]));
+                        m[i & 3] = fmaxf(m[i & 3], __uint_as_float(s[i]));
                 }
                 const float here = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 const bool moves = here > (top == -INFINITY ? top : top + slack);
@@ -876,7 +911,6 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                     top = here;
                     sum *= old;
                 }
-                tmem_wait_load(s[0]);
                 if (j != u.j0 && __any_sync(0xffffffffu, moves)) {
 #pragma unroll 1
                     for (int g = 0; g < S::DP / 16; ++g) {
@@ -895,28 +929,19 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                 // type asks: a relative error of at most half an ulp each; the
                 // sum is of the unrounded ones.
 #pragma unroll 1
-                for (int g = 0; g < 4; g += 2) {
+                for (int g = 0; g < 4; ++g) {
                     uint32_t w[16];
+                    tmem_load32(s, score_cols + 32 * g);
+                    tmem_wait_load(s);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (h == 0)
-                            tmem_load32(s[1], score_cols + 32 * (g + 1));
-                        else if (g == 0)
-                            tmem_load32(s[0], score_cols + 64);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = exp2_fast(fmaf(__uint_as_float(s[h][2 * i]), c, -shift));
-                            const float b = exp2_fast(fmaf(__uint_as_float(s[h][2 * i + 1]), c, -shift));
-                            part[2 * i & 3] += a;
-                            part[(2 * i + 1) & 3] += b;
-                            w[i] = pack16<S::BF16>(a, b);
-                        }
-                        tmem_store16(score_cols + 16 * (g + h), w);
-                        if (h == 0)
-                            tmem_wait_load(s[1]);
-                        else if (g == 0)
-                            tmem_wait_load(s[0]);
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = exp2_fast(fmaf(__uint_as_float(s[2 * i]), c, -shift));
+                        const float b = exp2_fast(fmaf(__uint_as_float(s[2 * i + 1]), c, -shift));
+                        part[2 * i & 3] += a;
+                        part[(2 * i + 1) & 3] += b;
+                        w[i] = pack16<S::BF16>(a, b);
                     }
+                    tmem_store16(score_cols + 16 * g, w);
                 }
                 sum += (part[0] + part[1]) + (part[2] + part[3]);
                 tmem_wait_store();
@@ -966,7 +991,7 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
         tmem_alloc<S::kCols>(smem_u32(&cta.misc->tmem));
     pdl_wait_prerequisite();
     pdl_launch_dependents();
-    const Place place = find_run<S::kThreads>(p, S::kUnitRows, gridDim.x, blockIdx.x, cta.misc->words);
+    const Place place = find_run<S::kThreads>(p, S::kUnitRows, gridDim.x, blockIdx.x, cta.misc->found);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -138,11 +138,21 @@ __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, int n, bool b_mn)
 // Shared-memory descriptor of an operand in 128-byte swizzled rows: blocks of
 // 8 rows x 128 bytes follow one another at 1024 bytes; `lead` is the distance
 // of the next 64 contiguous elements (only an operand with its M or N
-// dimension contiguous uses it).
-__device__ __forceinline__ uint64_t umma_desc(uint32_t smem, uint32_t lead)
+// dimension contiguous uses it).  In two steps, the address's half once per
+// tile and a constant offset per instruction: one thread issues every 64
+// cycles at best, and building the descriptor anew took it 175.
+__device__ __forceinline__ uint32_t umma_desc_low(uint32_t smem, uint32_t lead)
 {
-    return (uint64_t)((smem & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 |
-           (uint64_t)(1024u >> 4) << 32 | 1ull << 46 | 2ull << 61;
+    return smem >> 4 | (lead >> 4) << 16;
+}
+
+__device__ __forceinline__ uint64_t umma_desc(uint32_t low, uint32_t offset)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};"
+        : "=l"(d)
+        : "r"(low + (offset >> 4)), "n"((1024 >> 4) | 1 << 14 | 2 << 29));
+    return d;
 }
 
 // D (+)= A B, A and B in shared memory; one thread issues.
