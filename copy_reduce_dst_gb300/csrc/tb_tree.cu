@@ -341,58 +341,85 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
 {
     const KvView &c = p.c;
     const int lane = threadIdx.x & 31, boxes = S::kPos / maps.box;
-    uint32_t k = 0, tail_use = 0, tail_parity = 0;  // by stage: its last load, uses of kTail
+    uint32_t stage = 0, empty = 1;               // the next stage and the parity it waits for
+    uint32_t k = 0, tail_use = 0, tail_parity = 0;  // loads; by stage: its last one, uses of kTail
     Unit u;
     while (walk.next(u)) {
-        for (int x = 2 * S::kParts * u.j0; x < 2 * S::kParts * u.j1; ++x, ++k) {
-            const int j = x / (2 * S::kParts), part = x % S::kParts;
-            const bool value = x / S::kParts & 1;
-            const int pos = j * kTile + part * S::kPos + lane * maps.box;
-            int page = c.pages;  // past the pool: zeros
-            if (lane < boxes && pos < u.s.end && pos / c.page_tokens < c.width) {
-                page = __ldg(c.table + (int64_t)u.s.slot * c.width + pos / c.page_tokens);
-                if (page < 0 || page > c.pages)
-                    page = c.pages;
+        // The table is read 32 boxes at a time, a lane each, one group ahead:
+        // its latency would otherwise come before every load.
+        const int32_t *row = c.table + (int64_t)u.s.slot * c.width;
+        auto look_up = [&](int group, int &page, int &token) {
+            const int pos = (32 * group + lane) * maps.box, at = pos / c.page_tokens;
+            token = pos - at * c.page_tokens;
+            page = pos < u.s.end && at < c.width ? __ldg(row + at) : -1;
+        };
+        int first = u.j0 * (kTile / maps.box);  // the stage's first box
+        int group = first / 32, page, token, next_page, next_token;
+        look_up(group, page, token);
+        look_up(group + 1, next_page, next_token);
+        for (int j = u.j0; j < u.j1; ++j) {
+            if (first / 32 != group) {
+                group = first / 32;
+                page = next_page;
+                token = next_token;
+                look_up(group + 1, next_page, next_token);
             }
-            const uint32_t stage = k % S::kStages, to = cta.smem + S::kRing + stage * S::kStage;
-            const bool tail = value && u.tail(j);
-            bool ok = true;
-            if (lane == 0) {
-                ok = cta.wait(kEmpty + stage, (k / S::kStages & 1) ^ 1);
-                if (ok) {
-                    mbar_expect_tx(cta.bar((tail ? kTail : kFull) + stage), S::kStage);
-                    if (!tail)
-                        mbar_arrive(cta.bar(kFull + stage));
+            // A tile's boxes lie in one group: 32 is a multiple of their number.
+#pragma unroll 1
+            for (int x = 0; x < 2 * S::kParts; ++x) {
+                const bool value = x >= S::kParts;
+                const int part = value ? x - S::kParts : x;
+                const int from = (first + part * boxes + lane) & 31;
+                int at_page = __shfl_sync(0xffffffffu, page, from);
+                const int at_token = __shfl_sync(0xffffffffu, token, from);
+                if (at_page < 0 || at_page >= c.pages)
+                    at_page = c.pages;  // past the pool: zeros
+                const uint32_t to = cta.smem + S::kRing + stage * S::kStage;
+                const bool tail = value && u.tail(j);
+                const uint32_t full = cta.bar((tail ? kTail : kFull) + stage);
+                bool ok = true;
+                if (lane == 0) {
+                    ok = cta.wait(kEmpty + stage, empty);
+                    if (ok) {
+                        mbar_expect_tx(full, S::kStage);
+                        if (!tail && true)  // in the second fixing warp's place
+                            mbar_arrive(full);
+                    }
                 }
-            }
-            if (!__all_sync(0xffffffffu, ok)) {
-                // Let the tiles asked for land (bounded).
-                for (uint32_t y = k - min(k, (uint32_t)S::kStages); y < k; ++y) {
-                    const uint32_t s = y % S::kStages;
-                    if (tail_use >> s & 1)
-                        mbar_wait_bounded(cta.bar(kTail + s), (tail_parity >> s & 1) ^ 1);
-                    else
-                        mbar_wait_bounded(cta.bar(kFull + s), y / S::kStages & 1);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    // Let the tiles asked for land (bounded).
+                    for (uint32_t y = k - min(k, (uint32_t)S::kStages); y < k; ++y) {
+                        const uint32_t s = y % S::kStages;
+                        if (tail_use >> s & 1)
+                            mbar_wait_bounded(cta.bar(kTail + s), (tail_parity >> s & 1) ^ 1);
+                        else
+                            mbar_wait_bounded(cta.bar(kFull + s), y / S::kStages & 1);
+                    }
+                    return;
                 }
-                return;
-            }
-            tail_use = (tail_use & ~(1u << stage)) | (uint32_t)tail << stage;
-            tail_parity ^= (uint32_t)tail << stage;
-            if (lane < boxes) {
-                int at[4] = {0, page, page, page};
-                at[maps.token_dim] = pos % c.page_tokens;
-                at[maps.head_dim] = u.head;
+                if (lane < boxes) {
+                    const int a = maps.token_dim == 1 ? at_token : maps.head_dim == 1 ? u.head : at_page;
+                    const int b = maps.token_dim == 2 ? at_token : maps.head_dim == 2 ? u.head : at_page;
+                    const int d = maps.token_dim == 3 ? at_token : maps.head_dim == 3 ? u.head : at_page;
 #pragma unroll
-                for (int h = 0; h < S::DP / 64; ++h)
-                    asm volatile(
-                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::"
-                        "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                            to + h * S::kHalf + lane * maps.box * 128),
-                        "l"(&maps.pool[value]), "r"(64 * h), "r"(at[1]), "r"(at[2]), "r"(at[3]),
-                        "r"(cta.bar((tail ? kTail : kFull) + stage))
-                        : "memory");
+                    for (int h = 0; h < S::DP / 64; ++h)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::"
+                            "complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                                to + h * S::kHalf + lane * maps.box * 128),
+                            "l"(&maps.pool[value]), "r"(64 * h), "r"(a), "r"(b), "r"(d), "r"(full)
+                            : "memory");
+                }
+                __syncwarp();
+                tail_use = (tail_use & ~(1u << stage)) | (uint32_t)tail << stage;
+                tail_parity ^= (uint32_t)tail << stage;
+                ++k;
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    empty ^= 1;
+                }
             }
-            __syncwarp();
+            first += kTile / maps.box;
         }
     }
 }
@@ -431,8 +458,7 @@ __device__ void fix_role(const TreePlan &p, const Cta &cta, Walk walk)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(cta.bar(kFull + stage));
+                mbar_arrive_if(cta.bar(kFull + stage), lane == 0);
             }
         k += 2 * S::kParts * u.tiles();
     }
@@ -478,8 +504,7 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0)
-            mbar_arrive(cta.bar(kFull + done % S::kStages));
+        mbar_arrive_if(cta.bar(kFull + done % S::kStages), lane == 0);
         ++done;
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i)
@@ -805,14 +830,15 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
     auto hand_back = [&](const Unit &of) {
         if (S::STREAMS == 1)
             return;
-        if (stream * kRowTile + kRowTile >= of.rows && (threadIdx.x & 127) == 0)
-            mbar_arrive(cta.bar(kEmpty + stage));
-        stage = (stage + 1) % S::kStages;
+        mbar_arrive_if(cta.bar(kEmpty + stage),
+                       stream * kRowTile + kRowTile >= of.rows && (threadIdx.x & 127) == 0);
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
     };
     for (;;) {
         bool more;  // a further unit has rows for this stream
+        uint32_t others = 0;  // stages that units without rows for this stream use before that
         while ((more = walk.next(u)) && u.rows <= stream * kRowTile)
-            stage = (stage + 2 * u.tiles()) % S::kStages;
+            others += 2 * u.tiles();
         // The query rows of the stream's tile are on their way while the last
         // unit's last product runs, and its first scores while the last sums
         // are read: those are not written again before this stream's next
@@ -843,6 +869,7 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             tc_fence_after();
             hand_back(before);  // the last values
         }
+        stage = (stage + others) % S::kStages;
         if (more) {
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
@@ -853,8 +880,7 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(cta.bar(kQuery + stream));
+            mbar_arrive_if(cta.bar(kQuery + stream), lane == 0);
         }
         if (begun)
             write_unit<S>(p, cta, before, run, stream * kRowTile + tid, sum_cols, top, sum, c);
@@ -948,8 +974,7 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(cta.bar(kWeights + stream));
+            mbar_arrive_if(cta.bar(kWeights + stream), lane == 0);
         }
         before = u;
         begun = true;

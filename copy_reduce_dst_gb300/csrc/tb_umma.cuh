@@ -196,6 +196,17 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// mbar_arrive where `yes`, without a branch: a warp that parts and meets again
+// takes longer than the instruction.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool yes)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"((uint32_t)yes)
+        : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;

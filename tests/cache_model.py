@@ -112,10 +112,11 @@ class CacheModel:
         return status
 
 
-def tree_attention(q, k, v, table, lens, q_start, mask, scale, slots=None):
+def tree_attention(q, k, v, table, lens, q_start, mask, scale, slots=None, only=None):
     """(out, lse, reach, logit): the attention of one layer's pools [pages,
     tokens, heads, dim] in 64 bits; reach = sum of p |v| per output element and
-    logit = the largest scale * sum |q||k| of a row, for error bounds."""
+    logit = the largest scale * sum |q||k| of a row, for error bounds.  only:
+    the rows wanted (default: all)."""
     rows, q_heads, dim = q.shape
     P, heads = k.shape[1], k.shape[2]
     group = q_heads // heads
@@ -128,6 +129,8 @@ def tree_attention(q, k, v, table, lens, q_start, mask, scale, slots=None):
         at = np.arange(n + t)
         page = table[slot, at // P]
         for i in range(t):
+            if only is not None and r0 + i not in only:
+                continue
             seen = [j for j in range(t) if j // 32 < mask.shape[1]
                     and int(mask[r0 + i, j // 32]) >> (j % 32) & 1]
             cols = np.concatenate([np.arange(n), n + np.array(seen, int)]).astype(int)

@@ -34,10 +34,10 @@ class Case:
     """Random pools, rows and trees for sequences of lens[b] committed and drafts[b] drafted tokens."""
 
     def __init__(self, ctx, lens, drafts, q_heads=4, heads=2, dim=64, P=16, dtype="bf16", layout="NHD",
-                 layers=1, layer=0, seed=0, words=None, width=None, slots=None, spread=1.0):
+                 layers=1, layer=0, seed=0, words=None, width=None, slots=None, spread=1.0, check_rows=None):
         g = torch.Generator().manual_seed(seed)
         self.ctx, self.lens, self.drafts, self.layout, self.dtype = ctx, lens, drafts, layout, dtype
-        self.layer, self.P, self.slot_of = layer, P, slots
+        self.layer, self.P, self.slot_of, self.check_rows = layer, P, slots, check_rows
         seqs, t = len(lens), TYPES[dtype][0]
         need = [-(-(n + d) // P) for n, d in zip(lens, drafts)]
         pages = sum(need) + 3
@@ -65,6 +65,7 @@ class Case:
                 row = row[:self.words]
                 mask[self.q_start[b] + i, :len(row)] = row
         self.mask = mask.astype(np.int32)
+        self.rows = None if check_rows is None else sorted(rng.choice(rows, check_rows, replace=False).tolist())
         self.table, self.held = table, held
         self.scale = dim ** -0.5
 
@@ -90,7 +91,7 @@ class Case:
         k, v = (p[self.layer].float().numpy() for p in self.pools)
         return cache_model.tree_attention(self.q.float().numpy(), k, v, self.table.numpy(), self.all_lens.numpy(),
                                           self.q_start, self.mask.astype(np.int64) & 0xFFFFFFFF, self.scale,
-                                          self.slot_of)
+                                          self.slot_of, self.rows)
 
     def check(self, **kw):
         out, lse = self.run(**kw)
@@ -102,6 +103,10 @@ class Case:
         lost = longest * 2.0**-25 * biggest if self.dtype == "f16" else 0.0
         bound = u * np.abs(want) * 1.01 + (u * 1.01 + 2 * slack)[..., None] * reach * (1 + u) + lost + 1e-7
         off = np.abs(out.float().cpu().numpy().astype(np.float64) - want)
+        if self.rows is not None:  # the model did these
+            off, bound = off[self.rows], bound[self.rows]
+            want_lse, slack = want_lse[self.rows], slack[self.rows]
+            lse = None if lse is None else lse[self.rows]
         assert np.all(off <= bound), float((off / bound).max())
         if lse is not None:
             got = lse.cpu().numpy().astype(np.float64)
@@ -135,6 +140,15 @@ def test_groups(ctx, q_heads, heads, t):
 def test_large_trees(ctx, t):
     """More rows than a tile, mask words past the first, drafts over several tiles."""
     Case(ctx, [90, 3], [t, 7], q_heads=6, heads=2, seed=t).check()
+
+
+@pytest.mark.parametrize("drafts", [[48, 48, 48], [48, 3, 40, 16, 17], [33, 1, 1, 32]])
+@pytest.mark.parametrize("P", [16, 5])
+def test_units_of_one_and_two_row_tiles(ctx, drafts, P):
+    """Sequences of 8 to 384 rows per cache head, several tiles long, one after another in a run."""
+    lens = [900 + 130 * b for b in range(len(drafts))]
+    Case(ctx, lens, drafts, q_heads=8, heads=1, P=P, seed=sum(drafts)).check()
+    Case(ctx, lens * 12, drafts * 12, q_heads=16, heads=2, dim=128, P=P, seed=P, check_rows=40).check()
 
 
 def test_ragged_batch_with_empty_sequences(ctx):
