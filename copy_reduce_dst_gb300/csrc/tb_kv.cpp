@@ -250,8 +250,8 @@ int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream)
         return fail(ctx, TB_ENOTSUP, "tree_attention: head_dim %d is more than 128", c.head_dim);
     if (t->seqs > TB_TREE_MAX_SEQS)
         return fail(ctx, TB_ENOTSUP, "tree_attention: more than %d sequences", TB_TREE_MAX_SEQS);
-    if (t->rows > (1 << 29) || t->rows > INT_MAX / t->q_heads)
-        return fail(ctx, TB_ENOTSUP, "tree_attention: rows exceeds 2^29 or rows * q_heads 2^31 - 1");
+    if (t->rows > (1 << 29) || t->rows > (1 << 30) / t->q_heads)
+        return fail(ctx, TB_ENOTSUP, "tree_attention: rows exceeds 2^29 or rows * q_heads 2^30");
     // Work is counted in 32 bits, in tiles of 128 positions: what the longest
     // rows of the table and all query rows could make of it.
     const int64_t tiles = (int64_t)c.table_width * c.page_tokens / 128 + t->rows / 128 + 8;

@@ -95,6 +95,10 @@ class Case:
 
     def check(self, **kw):
         out, lse = self.run(**kw)
+        self.compare(out, lse)
+        return out, lse
+
+    def compare(self, out, lse):
         want, want_lse, reach, logit = self.want()
         u, dim = TYPES[self.dtype][1], self.q.shape[2]
         slack = (dim + 8) * 2.0**-24 * logit + 2.0**-20
@@ -113,7 +117,6 @@ class Case:
             np.testing.assert_array_equal(np.isneginf(got), np.isneginf(want_lse))
             real = ~np.isneginf(want_lse)
             assert np.all(np.abs(got - want_lse)[real] <= (slack + 2.0**-20 * (1 + np.abs(want_lse)))[real])
-        return out, lse
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
@@ -170,6 +173,63 @@ def test_one_long_sequence_split_over_the_gpu(ctx):
 
 def test_slots_layers_and_wide_tables(ctx):
     Case(ctx, [50, 20, 90], [4, 2, 6], slots=[4, 0, 2], layers=3, layer=2, width=40, seed=5).check()
+
+
+def test_keys_and_values_side_by_side(ctx):
+    """Pools that are views of one tensor, pages outermost, a gap after each token's heads."""
+    c = Case(ctx, [70, 130], [5, 9], q_heads=6, heads=3, layers=2, layer=1, seed=20)
+    want, want_lse = c.run()
+    cache, layer, q, q_start, mask, out, work = c.args
+    k = c.pools[0]
+    whole = torch.full((k.shape[1], 2, k.shape[0], k.shape[2], k.shape[3] + 1, k.shape[4]), float("nan"),
+                       dtype=k.dtype, device="cuda")
+    views = []
+    for i in range(2):
+        view = whole[:, i, :, :, :-1].permute(1, 0, 2, 3, 4)
+        view.copy_(c.pools[i])
+        views.append(view)
+    apart = tb.kv_cache(*views, *cache.tensors[2:])
+    again, lse = torch.full_like(out, 7.0), torch.empty_like(want_lse)
+    c.ctx.tree_attention(apart, layer, q, q_start, mask, again, work, scale=c.scale, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.equal(again, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("P", [16, 5])
+def test_missing_pages_read_as_zeros(ctx, P):
+    c = Case(ctx, [90, 40], [3, 2], P=P, seed=21)
+    zero = int(c.table[0, 1])  # a page that the table no longer names: the zeros of what is expected
+    c.table[0, 1], c.table[0, 3], c.table[1, 0] = -1, 2**30, c.pools[0].shape[1]
+    assert zero not in c.table
+    out, lse = c.run()
+    for pool in c.pools:
+        pool[:, zero] = 0.0
+    c.table[0, 1] = c.table[0, 3] = c.table[1, 0] = zero
+    c.compare(out, lse)
+
+
+def test_unknown_slots_see_nothing(ctx):
+    c = Case(ctx, [20, 30, 10], [2, 3, 1], slots=[0, 1, 2], seed=22)
+    c.run()
+    cache, layer, q, q_start, mask, out, work = c.args
+    slots = torch.tensor([0, 7, -1], dtype=torch.int32, device="cuda")
+    lse = torch.zeros(6, 4, device="cuda")
+    c.ctx.tree_attention(cache, layer, q, q_start, mask, out, work, scale=c.scale, lse=lse, seq_slots=slots)
+    torch.cuda.synchronize()
+    assert torch.all(out[2:] == 0) and torch.all(torch.isneginf(lse[2:])) and torch.isfinite(lse[:2]).all()
+
+
+def test_one_slot_read_by_several_sequences(ctx):
+    """Two trees after the same committed tokens: the drafts' places are shared, so the same drafts."""
+    c = Case(ctx, [50], [4], seed=23)
+    once, _ = c.run()
+    cache, layer, q, q_start, mask, out, work = c.args
+    twice = torch.empty(8, *q.shape[1:], dtype=q.dtype, device="cuda")
+    c.ctx.tree_attention(cache, layer, q.repeat(2, 1, 1), torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda"),
+                         mask.repeat(2, 1), twice, work, scale=c.scale,
+                         seq_slots=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert np.all(np.abs(twice.float().cpu().numpy() - once.repeat(2, 1, 1).float().cpu().numpy()) <= 2.0**-7)
 
 
 def test_rows_that_see_nothing(ctx):
