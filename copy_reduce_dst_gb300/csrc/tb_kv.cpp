@@ -110,6 +110,13 @@ int view_of(tb_ctx *ctx, const tb_kv_cache *cache, bool pools, bool table, const
     return TB_OK;
 }
 
+// Whether two arrays of n words share none.
+bool apart(const int32_t *a, const int32_t *b, uint64_t n)
+{
+    return reinterpret_cast<uintptr_t>(a) + 4 * n <= reinterpret_cast<uintptr_t>(b) ||
+           reinterpret_cast<uintptr_t>(b) + 4 * n <= reinterpret_cast<uintptr_t>(a);
+}
+
 int launched(tb_ctx *ctx, cudaError_t e, const char *what)
 {
     return e == cudaSuccess ? TB_OK : tb::cuda_fail(ctx, e, what);
@@ -134,8 +141,7 @@ int tb_kv_copy_pages(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *src, 
         return TB_OK;
     tb::DeviceScope scope(tb::ctx_device(ctx));
     return launched(ctx,
-                    tb::launch_copy_pages(v, src, dst, tokens, n, tb::ctx_num_sms(ctx),
-                                          tb::ctx_options(ctx).use_pdl != 0,
+                    tb::launch_copy_pages(v, src, dst, tokens, n, tb::ctx_options(ctx).use_pdl != 0,
                                           static_cast<cudaStream_t>(stream)),
                     "launch of the page copy");
 }
@@ -174,17 +180,13 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents, in
     if (v.slots > TB_KV_MAX_SLOTS)
         return fail(ctx, TB_ENOTSUP, "kv_fork: more than %d slots", TB_KV_MAX_SLOTS);
     const uint64_t rows = (uint64_t)v.slots * (uint64_t)v.width;
-    auto apart = [](const int32_t *a, const int32_t *b, uint64_t n) {
-        return reinterpret_cast<uintptr_t>(a) + 4 * n <= reinterpret_cast<uintptr_t>(b) ||
-               reinterpret_cast<uintptr_t>(b) + 4 * n <= reinterpret_cast<uintptr_t>(a);
-    };
     if (!apart(table_out, v.table, rows) || !apart(held_out, v.held, (uint64_t)v.slots) ||
         !apart(lens_out, v.lens, (uint64_t)v.slots))
         return fail(ctx, TB_EINVAL, "kv_fork: an output overlaps the array it replaces");
     tb::DeviceScope scope(tb::ctx_device(ctx));
     return launched(ctx,
                     tb::launch_kv_fork(v, parents, table_out, held_out, lens_out, status,
-                                       tb::ctx_num_sms(ctx), tb::ctx_options(ctx).use_pdl != 0,
+                                       tb::ctx_options(ctx).use_pdl != 0,
                                        static_cast<cudaStream_t>(stream)),
                     "launch of the fork");
 }
@@ -201,6 +203,8 @@ int tb_kv_compact(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *start, c
     if (!start || !count || !status || keep_stride < 0 || (keep_stride > 0 && !keep))
         return fail(ctx, TB_EINVAL,
                     "kv_compact: null start, keep, count or status, or keep_stride < 0");
+    if (!apart(start, v.lens, (uint64_t)v.slots) || !apart(count, v.lens, (uint64_t)v.slots))
+        return fail(ctx, TB_EINVAL, "kv_compact: start or count overlaps the cache's lens");
     if (v.slots > 65535)
         return fail(ctx, TB_ENOTSUP, "kv_compact: more than 65535 slots");
     tb::DeviceScope scope(tb::ctx_device(ctx));

@@ -21,13 +21,13 @@ struct KvView {
 
 // Launchers of tb_pages.cu.  pdl: programmatic dependent launch.
 cudaError_t launch_copy_pages(const KvView &c, const int32_t *src, const int32_t *dst,
-                              const int32_t *tokens, int32_t n, int num_sms, bool pdl,
+                              const int32_t *tokens, int32_t n, bool pdl,
                               cudaStream_t stream);
 cudaError_t launch_kv_resize(const KvView &c, const int32_t *capacity, int32_t *status, bool pdl,
                              cudaStream_t stream);
 cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *table_out,
-                           int32_t *held_out, int32_t *lens_out, int32_t *status, int num_sms,
-                           bool pdl, cudaStream_t stream);
+                           int32_t *held_out, int32_t *lens_out, int32_t *status, bool pdl,
+                           cudaStream_t stream);
 cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32_t *keep,
                               int32_t keep_stride, const int32_t *count, int32_t *status,
                               bool pdl, cudaStream_t stream);

@@ -149,8 +149,12 @@ __device__ __forceinline__ int pages_for(int tokens, int page_tokens)
 // them.  The counts are read again for the second pass: no page before its own
 // reader has handed it out changes between the two.
 // ---------------------------------------------------------------------------
-constexpr int kCluster = 16;       // CTAs for a large pool; one for a small one
-constexpr int kClusterPages = 16384;
+constexpr int kCluster = 16;
+// Pools of more pages than this are looked through by the cluster, others by one
+// CTA, which spares the cluster's start and barriers.  A call for 64 slots, one
+// CTA and 16: 1024 pages 5.2 and 6.4 us, 8192 6.6 and 8.4, 16384 8.6 and 8.4,
+// 65536 12.2 and 8.4, 1048576 51.2 and 12.2.
+constexpr int kClusterPages = 12288;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -493,8 +497,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 
 // The rest of the fork.  Blocks below row_blocks: entries of slot s's old row
 // (counts) and of its new one; the others: the part-filled page of a child that
-// took a fresh one, kTailLanes layers' keys or values each.
-constexpr int kTailLanes = 4;
+// took a fresh one, `each` of the layers' keys and values a CTA: one, for
+// latency's sake, while all are on the SMs at once, else four, whose checks are
+// then done once.  With 1 and 4 (half the slots copy): 4 slots of 2 layers 6.5
+// and 8.7 us, 64 of 4 10.0 and 11.5, 256 of 4 14.5 and 15.9, 256 of 16 25.6 and
+// 21.4.
+__host__ __device__ constexpr int tail_lanes(int slots, int lanes)
+{
+    return (int64_t)slots * lanes > 2048 ? 4 : 1;
+}
 
 __global__ void __launch_bounds__(kPageThreads)
     k_fork_rest(const KvView c, const int32_t *parents, int32_t *table_out, int32_t *held_out,
@@ -505,9 +516,10 @@ __global__ void __launch_bounds__(kPageThreads)
     pdl_wait_prerequisite();
     const bool refused = *status != 0;
     if ((int)blockIdx.x >= row_blocks) {
-        const int lanes = 2 * c.layers, groups = (lanes + kTailLanes - 1) / kTailLanes;
+        const int lanes = 2 * c.layers, each = tail_lanes(c.slots, lanes);
+        const int groups = (lanes + each - 1) / each;
         const int s = (blockIdx.x - row_blocks) / groups;
-        const int first = (blockIdx.x - row_blocks) % groups * kTailLanes;
+        const int first = (blockIdx.x - row_blocks) % groups * each;
         const int p = parents[s];
         if (refused || p < 0 || p == s)
             return;
@@ -517,7 +529,7 @@ __global__ void __launch_bounds__(kPageThreads)
         const int from = c.table[(int64_t)p * c.width + full];
         const int to = table_out[(int64_t)s * c.width + full];
         if (is_page(c, from) && is_page(c, to) && from != to)
-            for (int lane = first; lane < min(first + kTailLanes, lanes); ++lane)
+            for (int lane = first; lane < min(first + each, lanes); ++lane)
                 copy_page(c, pool_of(c, lane), from, to, (uint32_t)tail);
         return;
     }
@@ -631,7 +643,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 constexpr int kSet = 8;         // tokens requested at a time
 constexpr int kRing = 8;        // sets on their way to shared memory, where only their thread reads them
 constexpr int kLookAhead = 4;   // blocks of 32 list entries looked up, or in use
-constexpr int kFusedList = 256; // longest list that the moving CTAs check themselves
 
 // CHECK: no k_compact_check has run.
 template <bool CHECK>
@@ -764,10 +775,9 @@ cudaError_t launch(void (*kernel)(Args...), dim3 grid, int threads, size_t smem,
 }  // namespace
 
 cudaError_t launch_copy_pages(const KvView &c, const int32_t *src, const int32_t *dst,
-                              const int32_t *tokens, int32_t n, int num_sms, bool pdl,
+                              const int32_t *tokens, int32_t n, bool pdl,
                               cudaStream_t stream)
 {
-    (void)num_sms;
     const int64_t jobs = 2ll * c.layers * n;
     const unsigned grid = (unsigned)(jobs < (1 << 30) ? jobs : 1 << 30);
     return launch(k_copy_pages, dim3(grid), kPageThreads, 0, 1, pdl, stream, c, src, dst, tokens, jobs);
@@ -803,16 +813,15 @@ cudaError_t launch_kv_resize(const KvView &c, const int32_t *capacity, int32_t *
 }
 
 cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *table_out,
-                           int32_t *held_out, int32_t *lens_out, int32_t *status, int num_sms,
-                           bool pdl, cudaStream_t stream)
+                           int32_t *held_out, int32_t *lens_out, int32_t *status, bool pdl,
+                           cudaStream_t stream)
 {
-    (void)num_sms;
     const cudaError_t e = launch_plan(k_fork_plan<true>, k_fork_plan<false>, c, 2 * c.slots * sizeof(int),
                                       pdl, stream, c, parents, table_out, status);
     if (e != cudaSuccess)
         return e;
     const int per_row = (c.width + kPageThreads - 1) / kPageThreads, rows = c.slots * per_row;
-    const int groups = (2 * c.layers + kTailLanes - 1) / kTailLanes;
+    const int each = tail_lanes(c.slots, 2 * c.layers), groups = (2 * c.layers + each - 1) / each;
     return launch(k_fork_rest, dim3((unsigned)rows + (unsigned)(c.slots * groups)), kPageThreads, 0, 1, pdl,
                   stream, c, parents, table_out, held_out, lens_out, (const int32_t *)status, rows, per_row);
 }
@@ -823,7 +832,12 @@ cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32
 {
     const int64_t cols = 2ll * c.layers * c.heads * (c.row_bytes / 16);
     const dim3 grid((unsigned)((cols + 31) / 32), c.slots);
-    if (keep_stride <= kFusedList)
+    // Every moving CTA checks its slot's list, or one a slot does in a launch
+    // before: the first is quicker for a short list and few CTAs.  One CTA a
+    // list, and all: 32 CTAs, lists of 8 tokens 7.0 and 5.8 us, of 64 9.3 and
+    // 8.4, of 128 11.9 and 11.9, of 256 17.1 and 19.7; 256 CTAs, of 8 7.4 and
+    // 5.9; 1024, of 8 9.9 and 10.0, of 64 15.4 and 17.4; 8192, of 8 28.5 and 39.2.
+    if (keep_stride <= 128 && (int64_t)grid.x * grid.y <= 512)
         return launch(k_kv_compact<true>, grid, 32, 0, 1, pdl, stream, c, start, keep, keep_stride, count,
                       status);
     const cudaError_t e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start,

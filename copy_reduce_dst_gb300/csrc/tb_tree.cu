@@ -38,7 +38,6 @@ constexpr int kLoadWarps = 3;    // load by threads, or ...
 constexpr int kFixWarps = 2;     // ... one asks for tiles and two look drafts over
 constexpr int kJoinThreads = 256;
 constexpr int kUnitCost = 2;     // what a unit costs besides its tiles, in tiles
-constexpr int kJoinRows = 8;     // rows of a unit one CTA of k_tree_join takes
 
 struct Seq {
     int slot, row0, T, n, end, tiles, units;  // units per cache head
@@ -106,24 +105,13 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
     };
     Place r{};
     Seq s{};
-    int mine = 0, one = 0, count = 0;
+    int mine = 0, one = 0;
     for (int b = threadIdx.x; b < p.seqs; b += THREADS) {
         s = seq_of(p, b, unit_rows);
         mine += one = work_of(p, s);
-        count += s.units * p.c.heads;
     }
     int before = scan(mine, r.total);
     r.ctas = min(r.total, grid);
-    if (unit_rows > kRowTile) {
-        // Units of one sequence and head read the same keys and values.  Where
-        // nearly as many runs as there are SMs make whole numbers of runs a
-        // unit (of equal ones), those units read a tile at the same time, and
-        // one of them finds it in L2.
-        int units;
-        scan(count, units);
-        if (units <= grid && grid / units * units >= grid - grid / 16)
-            r.ctas = min(r.total, grid / units * units);
-    }
     if (c >= r.ctas)
         return r;
     r.each = r.total / r.ctas;
@@ -382,7 +370,7 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
                     ok = cta.wait(kEmpty + stage, empty);
                     if (ok) {
                         mbar_expect_tx(full, S::kStage);
-                        if (!tail && true)  // in the second fixing warp's place
+                        if (!tail)  // in the second fixing warp's place
                             mbar_arrive(full);
                     }
                 }
@@ -466,7 +454,10 @@ __device__ void fix_role(const TreePlan &p, const Cta &cta, Walk walk)
 
 // Any other page: each of three warps takes 16 rows of a stage at a time, its
 // lanes 16 bytes each, by asynchronous copies, and looks over its own drafts.
-constexpr int kInFlight = 2;  // stages behind the one being requested
+// (131072 tokens x 128 rows: 160 us in pages of 20 and 181 of one, 122 by
+// tensor maps in pages of 8; those, loaded this way, took 283 before stages were
+// handed on while the next one's place is waited for.)
+constexpr int kInFlight = 2;  // stages behind the one being requested; with 3: 212 us
 
 template <class S>
 __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
@@ -478,6 +469,8 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
     const int chunk = lane % kChunks;
     uint32_t k = 0;     // stages asked for
     uint32_t done = 0;  // stages handed over
+    // A stage has 4 or 8 blocks: the warp that takes most of them changes.
+    auto first_block = [&](uint32_t x) { return (int)((warp + x) % kLoadWarps); };
     struct Asked {
         int base, drafts, end, unit;  // positions drafts .. end - 1 of a value stage are drafts
     } asked[kInFlight + 1];
@@ -487,7 +480,7 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
         const Asked &a = asked[0];
         const uint32_t at = cta.smem + S::kRing + done % S::kStages * S::kStage;
         if (a.drafts < a.end && a.drafts < a.base + S::kPos && a.end > a.base) {
-            for (int block = warp; block < S::kPos / 16; block += kLoadWarps)
+            for (int block = first_block(done); block < S::kPos / 16; block += kLoadWarps)
                 for (int r = 0; r < 16; r += kLanesRows) {
                     const int row = block * 16 + r + lane / kChunks, pos = a.base + row;
                     if (pos >= a.drafts && pos < a.end) {
@@ -510,18 +503,32 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
         for (int i = 0; i < kInFlight; ++i)
             asked[i] = asked[i + 1];
     };
+    // The same of `flying` stages that may still be on their way.
+    auto hand_over_oldest = [&](uint32_t flying) {
+        if (flying == 1)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (flying == 2)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+        hand_over();
+    };
     bool ok = true;
     while (ok && walk.next(u)) {
         for (int x = 2 * S::kParts * u.j0; x < 2 * S::kParts * u.j1; ++x, ++k) {
             const int base = x / (2 * S::kParts) * kTile + x % S::kParts * S::kPos;
             const bool value = x / S::kParts & 1;
             const uint32_t stage = k % S::kStages, to = cta.smem + S::kRing + stage * S::kStage;
-            ok = lane != 0 || cta.wait(kEmpty + stage, (k / S::kStages & 1) ^ 1);
+            // While the stage's last readers are at work, what has landed is handed on.
+            const uint32_t parity = (k / S::kStages & 1) ^ 1;
+            while (k != done && !__all_sync(0xffffffffu, mbar_test_wait(cta.bar(kEmpty + stage), parity)))
+                hand_over_oldest(k - done);
+            ok = lane != 0 || cta.wait(kEmpty + stage, parity);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
             const char *pool = c.pool[value] + u.head * c.head_stride;
-            for (int block = warp; block < S::kPos / 16; block += kLoadWarps) {
+            for (int block = first_block(k); block < S::kPos / 16; block += kLoadWarps) {
                 int64_t at = -1;
                 const int pos = base + block * 16 + (lane & 15);
                 if (pos < u.s.end && pos / c.page_tokens < c.width) {
@@ -1064,25 +1071,26 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
 
 // ---------------------------------------------------------------------------
 // Joins the parts of the units that run ends cut: CTA (x, y) takes rows
-// kJoinRows y onwards of the unit whose first cut is run x + 1's start; a warp
+// rows_each y onwards of the unit whose first cut is run x + 1's start; a warp
 // per row, eight parts at a time, all of whose loads are under way before the
 // first is used.
 // ---------------------------------------------------------------------------
 template <class S>
-__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreePlan p, int ctas)
+__global__ void __launch_bounds__(kJoinThreads)
+    k_tree_join(const TreePlan p, int ctas, int rows_each)
 {
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     const Cut u = cuts_of<S>(p, ctas)[blockIdx.x + 1];
-    if ((int)blockIdx.y * kJoinRows >= u.rows)
+    if ((int)blockIdx.y * rows_each >= u.rows)
         return;
     const int lane = threadIdx.x & 31, parts = u.parts;
     constexpr int kPer = S::DP / 32, kSide = 8;
     const float *first = part_of<S>(p, 2 * blockIdx.x + 1);  // the unit begins in this run
     const int64_t pitch = 2 * part_floats(S::kUnitRows, S::DP);
 #pragma unroll 1
-    for (int row = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-         row < min((int)(blockIdx.y + 1) * kJoinRows, u.rows); row += kJoinThreads / 32) {
+    for (int row = blockIdx.y * rows_each + (threadIdx.x >> 5);
+         row < min((int)(blockIdx.y + 1) * rows_each, u.rows); row += kJoinThreads / 32) {
         float top = -INFINITY, sum = 0.0f, x[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
@@ -1234,8 +1242,13 @@ cudaError_t launch_shape(const TreePlan &p, int num_sms, bool pdl, cudaStream_t 
     if (e != cudaSuccess || ctas < 2)
         return e;
     const int rows = p.rows < S::kUnitRows / p.group ? p.rows * p.group : S::kUnitRows;
-    return launch(k_tree_join<S>, dim3(ctas - 1, (rows + kJoinRows - 1) / kJoinRows), kJoinThreads, 0, pdl,
-                  stream, p, ctas);
+    // Units of many parts want many CTAs, a row a warp; of few parts, fewer CTAs,
+    // two rows a warp.  With 8 and 16 rows a CTA: 8 units on 304 runs of 131072
+    // positions 109 and 114 us, one chat 12.1 and 12.9; 256 units on 304 runs
+    // (32 chats) 68.3 and 67.1, 512 on 304 65.6 and 63.3, 8 on 152 82.7 and 82.5.
+    const int each = (int64_t)p.seqs * p.c.heads * 16 > ctas ? 16 : 8;
+    return launch(k_tree_join<S>, dim3(ctas - 1, (rows + each - 1) / each), kJoinThreads, 0, pdl, stream, p,
+                  ctas, each);
 }
 
 template <int DP, bool BF16>

@@ -633,7 +633,8 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
 /* Squeezes kept tokens together: in slot s, for i in [0, count[s]), the token
    at start[s] + keep[s * keep_stride + i] moves to start[s] + i, in every
    layer, keys and values, as if in order of i; then lens[s] = start[s] +
-   count[s].  keep ascends strictly.  With start = the committed length and
+   count[s].  keep ascends strictly; start and count must not overlap lens.
+   With start = the committed length and
    keep = the accepted path of a draft tree this commits that path; with start
    = 0 it drops the tokens not listed.  Pages past the new length stay with
    the slot (tb_kv_resize gives them back).  A negative count leaves its slot
@@ -678,7 +679,12 @@ typedef struct {
    not reach the result, whatever their bits.  Sums, maxima and the output
    accumulate in 32 bits.  The result depends on the inputs alone: two calls
    give the same bits.  Every position needs a page in the slot's row; what
-   has none reads as zeros. */
+   has none reads as zeros.
+   Limits (TB_ENOTSUP past them): rows * q_heads up to 2^30, and the calls that
+   table_width and rows would allow have less than 2^31 tiles of 128 positions.
+   Expired waits: when a bounded wait inside the kernel runs out (option
+   kernel_wait_ns), the call's outputs are undefined; the context's first tree
+   attention after that has happened returns TB_ETIMEOUT and enqueues nothing. */
 int tb_tree_attention(tb_ctx *ctx, const tb_tree *t, tb_stream stream);
 
 /* Bytes of workspace tb_tree_attention needs on this context's device for a

@@ -270,6 +270,19 @@ def test_compact_long_list(ctx):
     x.check()
 
 
+def test_compact_short_lists_of_many_slots(ctx):
+    slots, P = 150, 5
+    x = Cache(layers=8, slots=slots, width=5, pages=5 * slots, P=P, heads=2, dim=64)
+    x.resize(ctx, [25] * slots)
+    x.set_lens([11] * slots)
+    g = np.random.default_rng(4)
+    keep = np.sort([g.permutation(14)[:4] for _ in range(slots)], axis=1)
+    keep[7] = [0, 3, 3, 4]  # does not ascend
+    keep[8] = [0, 2, 4, 14]  # past the slot's pages
+    x.compact(ctx, [11] * slots, keep, g.integers(-1, 5, slots).tolist())
+    x.check()
+
+
 def test_compact_refusals(ctx):
     x = Cache(slots=6, width=4, pages=40, P=4)
     x.resize(ctx, [16] * 5 + [0])
@@ -374,6 +387,8 @@ def test_refusals(ctx):
         ctx.handle, x.c.ref, many.data_ptr(), one.data_ptr(), None), ""))
     undo()
     refused(tb.TB_EINVAL, ctx.kv_fork, x.c, many, x.table, torch.empty_like(x.held), torch.empty_like(x.lens), one)
+    refused(tb.TB_EINVAL, ctx.kv_compact, x.c, x.lens, many[:, None].contiguous(), many, torch.empty_like(many))
+    refused(tb.TB_EINVAL, ctx.kv_compact, x.c, many, many[:, None].contiguous(), x.lens, torch.empty_like(many))
     refused(tb.TB_EINVAL, ctx.kv_fork, x.c, many, torch.empty_like(x.table), x.held, torch.empty_like(x.lens), one)
     with pytest.raises(ValueError):
         ctx.kv_resize(x.c, dev(np.zeros(4, np.int32)), one)

@@ -133,7 +133,7 @@ def test_lengths_about_tiles(ctx, n, t):
     Case(ctx, [n], [t], seed=n + t).check()
 
 
-@pytest.mark.parametrize("q_heads,heads", [(1, 1), (6, 6), (7, 1), (10, 2), (64, 4), (40, 8)])
+@pytest.mark.parametrize("q_heads,heads", [(1, 1), (6, 6), (7, 1), (10, 2), (64, 4), (40, 8), (129, 1), (300, 2)])
 @pytest.mark.parametrize("t", [1, 5, 16])
 def test_groups(ctx, q_heads, heads, t):
     Case(ctx, [70, 200], [t, t], q_heads=q_heads, heads=heads, dim=128, seed=q_heads).check()
