@@ -95,6 +95,9 @@ __device__ __forceinline__ char *pool_of(const KvView &c, int32_t lane)
     return (lane & 1 ? c.pool[1] : c.pool[0]) + (lane >> 1) * c.layer_stride;
 }
 
+// A CTA per page, layer and pool.  Bound by HBM: 1000 pages of 32 KB in 16 layers
+// 302 us (6.9 TB/s read and written; one load a thread in flight 319 us), 8
+// pages in 2 layers 2.8 us, a launch's latency.
 __global__ void __launch_bounds__(kPageThreads)
     k_copy_pages(const KvView c, const int32_t *src, const int32_t *dst, const int32_t *tokens,
                  int64_t jobs)
@@ -146,8 +149,10 @@ __device__ __forceinline__ int pages_for(int tokens, int page_tokens)
 // before each one: the pool's counts are split over the CTAs of one cluster
 // (their SMs read together; totals meet in distributed shared memory, so no
 // scratch memory is needed), and each warp counts, then hands out, a run of
-// them.  The counts are read again for the second pass: no page before its own
-// reader has handed it out changes between the two.
+// them: 32 neighbouring pages a lane, as bits of a word kept in a register from
+// the first pass to the second.  Bound by the chain of its steps, not by its
+// bytes (512 slots x 4096 entries, 8.4 MB of counts: 24 us a call; with one CTA
+// 1670, a page a lane and every count read twice 65).
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 16;
 // Pools of more pages than this are looked through by the cluster, others by one
@@ -329,6 +334,9 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x)
     return lo;
 }
 
+// New pages for slot s: need - held where that is positive; a prefix sum over the
+// slots turns a free page's rank into its slot and entry.  16 slots 6.3 us: two
+// dependent reads, three scans of the block and the writes.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kPlanThreads, 1)
     k_kv_resize(const KvView c, const int32_t *capacity, int32_t *status)
@@ -422,7 +430,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Fork
+// Fork, in two launches: which slots take a fresh page has to be known for all
+// before pages are handed out; the counts, rows and page tails then go to as many
+// CTAs as there are.  Bound by the two launches' latency: 4 beams 6.6 us, 32 x 8
+// beams of 4007 tokens 14.9 (20 MB of tails and rows, 6.1 us of HBM).
 // ---------------------------------------------------------------------------
 
 // Decides which children take a fresh page for the part-filled one and takes
@@ -581,8 +592,15 @@ __global__ void __launch_bounds__(kPageThreads)
 // Compact.  A token's rows of one layer are split into 16-byte columns; a
 // thread walks one column through the slot's list, reading ahead of what it
 // writes: every later source lies past every destination written so far (keep
-// ascends, so keep[i] >= i), so no column needs another's progress.  A CTA is
-// one warp: the columns of a few slots still spread over all SMs.
+// ascends, so keep[i] >= i), so no column needs another's progress.  The warps
+// of a CTA share 32 columns, and a round of the list: eight tokens a warp, read
+// by all before any is written.
+//
+// Bound by HBM where there are many columns: 8 slots x 8 layers, heads of 256
+// bytes first, 2048 to 4096 of 8192 tokens kept, 282 us (1.6 GB, 5.7 TB/s); 32
+// slots x 32 layers, every other of 8192 tokens, 4.94 ms (34 GB, 7.0 TB/s).  By
+// each round's chain of instructions where there are few: a slot of 4 layers of
+// 8 heads, 4096 tokens, 67 us, with one warp a CTA 195.
 // ---------------------------------------------------------------------------
 
 // Whether slot s's list may be carried out, as tb_kv_compact's status; the
@@ -641,25 +659,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
 }
 
 constexpr int kSet = 8;         // tokens requested at a time
-constexpr int kRing = 8;        // sets on their way to shared memory, where only their thread reads them
 constexpr int kLookAhead = 4;   // blocks of 32 list entries looked up, or in use
 
+// A warp's sets on their way to shared memory, where only their thread reads
+// them, and its list entries.
+template <int RING>
+struct Moving {
+    uint4 ring[RING][kSet][32];
+    int64_t from[kLookAhead][32], to[kLookAhead][32];
+};
+
 // CHECK: no k_compact_check has run.
-template <bool CHECK>
-__global__ void __launch_bounds__(32)
+template <bool CHECK, int WARPS, int RING>
+__global__ void __launch_bounds__(32 * WARPS)
     k_kv_compact(const KvView c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
                  const int32_t *count, int32_t *status)
 {
-    __shared__ __align__(16) uint4 ring[kRing][kSet][32];
-    __shared__ __align__(16) int64_t from[kLookAhead][32], to[kLookAhead][32];
+    extern __shared__ __align__(16) unsigned char raw[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto &[ring, from, to] = reinterpret_cast<Moving<RING> *>(raw)[warp];
     pdl_launch_dependents();
     pdl_wait_prerequisite();
-    const int s = blockIdx.y, n = count[s], P = c.page_tokens, lane = threadIdx.x;
+    const int s = blockIdx.y, n = count[s], P = c.page_tokens;
     const int64_t first = start[s];
     const int32_t *list = keep + (int64_t)s * keep_stride, *row = c.table + (int64_t)s * c.width;
     if (CHECK) {
         const int verdict = n < 0 ? 0 : compact_verdict(c, s, first, list, n, keep_stride);
-        if (blockIdx.x == 0 && lane == 0) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
             status[s] = verdict;
             if (n >= 0 && !verdict)
                 c.lens[s] = (int32_t)(first + n);
@@ -679,23 +705,26 @@ __global__ void __launch_bounds__(32)
         const int64_t half = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
         base = pool_of(c, (int32_t)half) + in / cols * c.head_stride + in % cols * 16;
     }
+    // A warp's block: its sets of four rounds, in each of which the CTA's warps
+    // take WARPS sets in turn.
+    auto index = [&](int block) { return kSet * (WARPS * (4 * block + lane / kSet) + warp) + lane % kSet; };
     // Looking up a block of 32 entries takes two dependent loads; both are
     // under way long before the block's tokens are requested.
     auto entry = [&](int block) {
-        const int i = 32 * block + lane;
+        const int i = index(block);
         return i < n ? list[i] : 0;
     };
     auto pages = [&](int block, int k) {
-        const int i = 32 * block + lane;
+        const int i = index(block);
         return i < n ? int2{row[(first + k) / P], row[(first + i) / P]} : int2{0, 0};
     };
     auto keep_block = [&](int block, int k, int2 page) {
-        const int64_t f = first + k, t = first + 32 * block + lane;
-        const bool moves = 32 * block + lane < n && f != t;
+        const int64_t f = first + k, t = first + index(block);
+        const bool moves = index(block) < n && f != t;
         from[block % kLookAhead][lane] = moves ? page.x * c.page_stride + f % P * c.token_stride : -1;
         to[block % kLookAhead][lane] = moves ? page.y * c.page_stride + t % P * c.token_stride : -1;
     };
-    auto places = [&](const int64_t(&of)[kLookAhead][32], int set, int64_t(&x)[kSet]) {
+    auto places = [&](int64_t(&of)[kLookAhead][32], int set, int64_t(&x)[kSet]) {
         const int4 *p = reinterpret_cast<const int4 *>(&of[set / 4 % kLookAhead][set % 4 * kSet]);
 #pragma unroll
         for (int u = 0; u < kSet / 2; ++u)
@@ -708,7 +737,7 @@ __global__ void __launch_bounds__(32)
         for (int u = 0; u < kSet; ++u)
             if (f[u] >= 0 && real)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(&ring[set % kRing][u][lane])),
+                                 smem_u32(&ring[set % RING][u][lane])),
                              "l"(base + f[u])
                              : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -720,9 +749,9 @@ __global__ void __launch_bounds__(32)
     int k2 = entry(2), k3 = entry(3);
     int2 p2 = pages(2, k2);
     __syncwarp();
-    for (int k = 0; k < kRing - 1; ++k)
+    for (int k = 0; k < RING - 1; ++k)
         request(k);
-    const int sets = (n + kSet - 1) / kSet;
+    const int sets = (n + kSet * WARPS - 1) / (kSet * WARPS);
     for (int k = 0; k < sets; ++k) {
         if (k % 4 == 0) {  // a block of four sets begins; requests reach into the second after it
             const int block = k / 4;
@@ -732,14 +761,16 @@ __global__ void __launch_bounds__(32)
             k3 = entry(block + 4);
             __syncwarp();
         }
-        request(k + kRing - 1);
+        request(k + RING - 1);
         int64_t d[kSet];
         uint4 v[kSet];
         places(to, k, d);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
 #pragma unroll
         for (int u = 0; u < kSet; ++u)
-            v[u] = ring[k % kRing][u][lane];
+            v[u] = ring[k % RING][u][lane];
+        if (WARPS > 1)  // what this round's sets write has been read
+            __syncthreads();
 #pragma unroll
         for (int u = 0; u < kSet; ++u)
             if (d[u] >= 0 && real)
@@ -826,26 +857,53 @@ cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *tab
                   stream, c, parents, table_out, held_out, lens_out, (const int32_t *)status, rows, per_row);
 }
 
+namespace {
+
+template <int WARPS, int RING>
+cudaError_t launch_compact(const KvView &c, const int32_t *start, const int32_t *keep, int32_t keep_stride,
+                           const int32_t *count, int32_t *status, dim3 grid, bool pdl, cudaStream_t stream)
+{
+    // Every moving CTA checks its slot's list, or one a slot does in a launch
+    // before, which costs 1.5 us but is done once.  All, and one: 128 CTAs and
+    // lists of 8 tokens 5.3 and 6.8 us, of 64 6.7 and 7.8, of 256 11.0 and 11.9;
+    // 256 CTAs, of 128 10.4 and 10.6, of 256 16.6 and 15.1; 512, of 64 10.9 and
+    // 10.7, of 128 15.5 and 13.8; 1024, of 8 9.8 and 9.8, of 64 17.1 and 15.0.
+    const bool check = keep_stride <= 256 && (int64_t)grid.x * grid.y * keep_stride <= 32768;
+    void (*kernel)(KvView, const int32_t *, const int32_t *, int32_t, const int32_t *, int32_t *) =
+        check ? k_kv_compact<true, WARPS, RING> : k_kv_compact<false, WARPS, RING>;
+    constexpr int bytes = WARPS * sizeof(Moving<RING>);
+    cudaError_t e = cudaSuccess;
+    if (bytes > 40 * 1024)
+        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && !check)
+        e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start, keep,
+                   keep_stride, count, status);
+    if (e != cudaSuccess)
+        return e;
+    return launch(kernel, grid, 32 * WARPS, bytes, 1, pdl, stream, c, start, keep, keep_stride, count,
+                  status);
+}
+
+}  // namespace
+
 cudaError_t launch_kv_compact(const KvView &c, const int32_t *start, const int32_t *keep,
                               int32_t keep_stride, const int32_t *count, int32_t *status,
                               bool pdl, cudaStream_t stream)
 {
     const int64_t cols = 2ll * c.layers * c.heads * (c.row_bytes / 16);
     const dim3 grid((unsigned)((cols + 31) / 32), c.slots);
-    // Every moving CTA checks its slot's list, or one a slot does in a launch
-    // before: the first is quicker for a short list and few CTAs.  One CTA a
-    // list, and all: 32 CTAs, lists of 8 tokens 7.0 and 5.8 us, of 64 9.3 and
-    // 8.4, of 128 11.9 and 11.9, of 256 17.1 and 19.7; 256 CTAs, of 8 7.4 and
-    // 5.9; 1024, of 8 9.9 and 10.0, of 64 15.4 and 17.4; 8192, of 8 28.5 and 39.2.
-    if (keep_stride <= 128 && (int64_t)grid.x * grid.y <= 512)
-        return launch(k_kv_compact<true>, grid, 32, 0, 1, pdl, stream, c, start, keep, keep_stride, count,
-                      status);
-    const cudaError_t e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start,
-                                 keep, keep_stride, count, status);
-    if (e != cudaSuccess)
-        return e;
-    return launch(k_kv_compact<false>, grid, 32, 0, 1, pdl, stream, c, start, keep, keep_stride, count,
-                  status);
+    const int64_t ctas = (int64_t)grid.x * grid.y;
+    // More warps a CTA shorten a list's walk; fewer let more CTAs share an SM and
+    // get to work sooner.  With 1, 4 and 8 warps: 128 CTAs, lists of 8 tokens 6.0,
+    // 5.5 and 5.2 us, of 1024 55.9, 30.6 and 24.1; 256 CTAs, of 8 5.9, 5.7 and
+    // 8.9, of 1024 66.9, 53.4 and 51.9; 1024, of 8 9.7, 11.0 and 18.3, of 128
+    // 25.4, 23.2 and 33.1, of 512 101, 91 and 91, of 4096 707, 665 and 646; 8192,
+    // of 8 28.4, 44.0 and 106, of 4096 5005, 4969 and 4946.
+    if (keep_stride >= 512)
+        return launch_compact<8, 4>(c, start, keep, keep_stride, count, status, grid, pdl, stream);
+    if (keep_stride >= 128 || ctas <= 304)
+        return launch_compact<4, 4>(c, start, keep, keep_stride, count, status, grid, pdl, stream);
+    return launch_compact<1, 8>(c, start, keep, keep_stride, count, status, grid, pdl, stream);
 }
 
 }  // namespace tb
