@@ -31,13 +31,29 @@ using namespace dev;
 // stores hide the other's, which is what short sequences need; and with two
 // streams, one CTA on an SM: both row tiles use the same keys and values, which
 // halves what has to come from L2 when there are more than 128 rows.
+//
+// The mathematics: with m the running maximum of a row's scores s_j (scaled) and
+// l = sum exp(s_j - m), o = sum exp(s_j - m) v_j over the positions so far, a new
+// maximum m' multiplies l and o by exp(m - m'); parts of one row (m, l, o) are
+// joined the same way, and out = o / l, lse = m + ln l.  Powers are of two,
+// scale * log2 e being part of the exponent's factor.
+//
+// What bounds it: up to about 128 rows a cache head, the keys and values from
+// HBM (8 sequences of 32768 positions, 32 rows: 174 us, 6.2 TB/s; 32 sequences
+// of up to 4096, 128 rows: 66 us, 4.1 TB/s, of which the start, the uneven ends
+// of the runs and the join are some 15); above, each stream's chain of scores,
+// maximum, weights and sums (131072 positions, 512 rows in two streams: 244 us,
+// 1130 TFLOP/s, tensor pipe 46% busy); for small calls the two launches and one
+// tile's chain (500 positions, 32 rows: 11 us).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;       // positions of a tile
 constexpr int kRowTile = 128;    // rows of one matrix instruction
 constexpr int kLoadWarps = 3;    // load by threads, or ...
 constexpr int kFixWarps = 2;     // ... one asks for tiles and two look drafts over
 constexpr int kJoinThreads = 256;
-constexpr int kUnitCost = 2;     // what a unit costs besides its tiles, in tiles
+// What a unit costs besides its tiles, in tiles.  With 0, 1, 2, 3 and 4: 32 chats
+// 73, 69, 68, 69 and 69 us, 96 short ones 66, 53, 52, 53 and 54.
+constexpr int kUnitCost = 2;
 
 struct Seq {
     int slot, row0, T, n, end, tiles, units;  // units per cache head
@@ -315,7 +331,10 @@ __device__ __forceinline__ bool clean(uint32_t &pair)
 // The order in which the products use them: the keys of a tile, its values, the
 // keys of the next.
 
-// Pages of a multiple of 8 tokens: one lane per box of `box` positions (the
+// Pages of a multiple of 8 tokens (a box has to begin at a multiple of 1024 bytes
+// of a swizzled tile, eight rows; by threads the same pages take two to three
+// times as long: 131072 positions, 128 rows in pages of 16 300 us, by boxes 110;
+// 32 chats in pages of 32 168 and 66): one lane per box of `box` positions (the
 // largest power of two that divides a page, at most a tile), by tensor maps of
 // (dim, token, head, page); positions without a page read as zeros.
 struct Maps {
@@ -1070,7 +1089,9 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of the units that run ends cut: CTA (x, y) takes rows
+// Joins the parts of the units that run ends cut, o and l by the powers of two of
+// their maxima's distance to the largest (some 5 us after 32 chats' 128 rows x 300
+// parts, 3 of them its launch and first loads): CTA (x, y) takes rows
 // rows_each y onwards of the unit whose first cut is run x + 1's start; a warp
 // per row, eight parts at a time, all of whose loads are under way before the
 // first is used.
@@ -1254,6 +1275,10 @@ cudaError_t launch_shape(const TreePlan &p, int num_sms, bool pdl, cudaStream_t 
 template <int DP, bool BF16>
 cudaError_t launch_dim(const TreePlan &p, int num_sms, bool pdl, cudaStream_t stream)
 {
+    // By the mean rows of a sequence and cache head.  8 sequences of 8192, one
+    // stream and two: 64 rows 62 and 73 us, 128 71 and 76, 136 107 and 80, 192
+    // 110 and 83, 256 115 and 91, 384 159 and 143, 1024 338 and 272; 64 sequences
+    // of up to 1000, 8 to 512 rows 113 and 104.
     if ((int64_t)p.rows * p.group > (int64_t)kRowTile * p.seqs)
         return launch_shape<Shape<DP, BF16, 2>>(p, num_sms, pdl, stream);
     return launch_shape<Shape<DP, BF16, 1>>(p, num_sms, pdl, stream);

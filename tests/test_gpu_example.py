@@ -14,6 +14,8 @@ if not torch.cuda.is_available():
 from copy_reduce_dst_gb300 import _build  # noqa: E402
 
 _build.build()
+from copy_reduce_dst_gb300 import tb  # noqa: E402
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -31,3 +33,16 @@ def test_tree_decode_agrees_with_plain_greedy_decoding():
         # their size and not always the same way: sqrt(2 * 12) 2^-8 of the logits'
         # spread, twice (a difference), three deviations.  A wrong token is off by two.
         assert float((best - taken).max()) <= 0.12 * float(logits.std())
+
+
+def test_readme_cache_example_runs():
+    text = open(os.path.join(ROOT, "README.md")).read()
+    code = text.split("```python")[2].split("```")[0]
+    scope = {"torch": torch, "tb": tb}
+    exec(compile(code, "README.md", "exec"), scope)
+    torch.cuda.synchronize()
+    assert scope["status"].tolist() == [0, 0, 0, 0]
+    table, held, lens = scope["new"]
+    assert lens.tolist() == [39, 39, 39, 0] and held.tolist() == [3, 3, 3, 0]
+    assert table[1, :2].tolist() == table[0, :2].tolist() and int(table[1, 2]) != int(table[0, 2])
+    assert scope["out"].isfinite().all()
