@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kPageThreads)
 // by all before any is written.
 //
 // Bound by HBM where there are many columns: 8 slots x 8 layers, heads of 256
-// bytes first, 2048 to 4096 of 8192 tokens kept, 282 us (1.6 GB, 5.7 TB/s); 32
+// bytes first, some 3400 of 8192 tokens kept, 282 us (1.78 GB, 6.3 TB/s); 32
 // slots x 32 layers, every other of 8192 tokens, 4.94 ms (34 GB, 7.0 TB/s).  By
 // each round's chain of instructions where there are few: a slot of 4 layers of
 // 8 heads, 4096 tokens, 67 us, with one warp a CTA 195.
