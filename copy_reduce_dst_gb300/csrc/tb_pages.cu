@@ -593,13 +593,13 @@ __global__ void __launch_bounds__(kPageThreads)
 // thread walks one column through the slot's list, reading ahead of what it
 // writes: every later source lies past every destination written so far (keep
 // ascends, so keep[i] >= i), so no column needs another's progress.  The warps
-// of a CTA share 32 columns, and a round of the list: eight tokens a warp, read
-// by all before any is written.
+// of a CTA share 32 columns, and take eight tokens of the list each in turn, all
+// of which are read before any is written.
 //
 // Bound by HBM where there are many columns: 8 slots x 8 layers, heads of 256
 // bytes first, some 3400 of 8192 tokens kept, 282 us (1.78 GB, 6.3 TB/s); 32
 // slots x 32 layers, every other of 8192 tokens, 4.94 ms (34 GB, 7.0 TB/s).  By
-// each round's chain of instructions where there are few: a slot of 4 layers of
+// each turn's chain of instructions where there are few: a slot of 4 layers of
 // 8 heads, 4096 tokens, 67 us, with one warp a CTA 195.
 // ---------------------------------------------------------------------------
 
@@ -705,8 +705,7 @@ __global__ void __launch_bounds__(32 * WARPS)
         const int64_t half = col / ((int64_t)c.heads * cols), in = col % ((int64_t)c.heads * cols);
         base = pool_of(c, (int32_t)half) + in / cols * c.head_stride + in % cols * 16;
     }
-    // A warp's block: its sets of four rounds, in each of which the CTA's warps
-    // take WARPS sets in turn.
+    // A warp's block: its sets of four turns.
     auto index = [&](int block) { return kSet * (WARPS * (4 * block + lane / kSet) + warp) + lane % kSet; };
     // Looking up a block of 32 entries takes two dependent loads; both are
     // under way long before the block's tokens are requested.
@@ -769,7 +768,7 @@ __global__ void __launch_bounds__(32 * WARPS)
 #pragma unroll
         for (int u = 0; u < kSet; ++u)
             v[u] = ring[k % RING][u][lane];
-        if (WARPS > 1)  // what this round's sets write has been read
+        if (WARPS > 1)  // what the sets of this turn write has been read
             __syncthreads();
 #pragma unroll
         for (int u = 0; u < kSet; ++u)
