@@ -871,14 +871,14 @@ cudaError_t launch_compact(const KvView &c, const int32_t *start, const int32_t 
     void (*kernel)(KvView, const int32_t *, const int32_t *, int32_t, const int32_t *, int32_t *) =
         check ? k_kv_compact<true, WARPS, RING> : k_kv_compact<false, WARPS, RING>;
     constexpr int bytes = WARPS * sizeof(Moving<RING>);
-    cudaError_t e = cudaSuccess;
-    if (bytes > 40 * 1024)
-        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && !check)
-        e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start, keep,
-                   keep_stride, count, status);
-    if (e != cudaSuccess)
-        return e;
+    if (resident_ctas((const void *)kernel, 32 * WARPS, bytes) < 1)  // once a kernel and device; allows the memory
+        return cudaErrorInvalidConfiguration;
+    if (!check) {
+        const cudaError_t e = launch(k_compact_check, dim3(c.slots), kPlanThreads, 0, 1, pdl, stream, c, start,
+                                     keep, keep_stride, count, status);
+        if (e != cudaSuccess)
+            return e;
+    }
     return launch(kernel, grid, 32 * WARPS, bytes, 1, pdl, stream, c, start, keep, keep_stride, count,
                   status);
 }
