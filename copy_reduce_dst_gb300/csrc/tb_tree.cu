@@ -40,8 +40,8 @@ using namespace dev;
 //
 // What bounds it: up to about 128 rows a cache head, the keys and values from
 // HBM (8 sequences of 32768 positions, 32 rows: 174 us, 6.2 TB/s; 32 sequences
-// of up to 4096, 128 rows: 66 us, 4.1 TB/s, of which the start, the uneven ends
-// of the runs and the join are some 15); above, each stream's chain of scores,
+// of up to 4096, 128 rows: 63 us, 4.3 TB/s; 40 us of that at the copy rate, 6 for
+// the join, the rest start and uneven ends of the runs); above, each stream's chain of scores,
 // maximum, weights and sums (131072 positions, 512 rows in two streams: 244 us,
 // 1130 TFLOP/s, tensor pipe 46% busy); for small calls the two launches and one
 // tile's chain (500 positions, 32 rows: 11 us).
@@ -1120,78 +1120,91 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
 
 // ---------------------------------------------------------------------------
 // Joins the parts of the units that run ends cut, o and l by the powers of two of
-// their maxima's distance to the largest (some 5 us after 32 chats' 128 rows x 300
-// parts, 3 of them its launch and first loads): CTA (x, y) takes rows
-// rows_each y onwards of the unit whose first cut is run x + 1's start; a warp
-// per row, eight parts at a time, all of whose loads are under way before the
-// first is used.
+// their maxima's distance to the largest: CTA (x, y) takes the y-th rows of the
+// unit whose first cut is run x + 1's start.  DP / 4 lanes read a row, 16 bytes
+// each, ROWS rows and SIDE parts of them at a time, all of whose loads are under
+// way before the first is used.  Bound by those loads' latency, from L2: of the 63
+// us of 32 chats it takes 6 (up to 40 MB of parts).
 // ---------------------------------------------------------------------------
-template <class S>
-__global__ void __launch_bounds__(kJoinThreads)
-    k_tree_join(const TreePlan p, int ctas, int rows_each)
+template <class S, int ROWS>
+constexpr int kJoinRows = kJoinThreads / (S::DP / 4) * ROWS;  // rows of a CTA
+
+template <class S, int ROWS, int SIDE>
+__global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreePlan p, int ctas)
 {
     pdl_launch_dependents();
     pdl_wait_prerequisite();
     const Cut u = cuts_of<S>(p, ctas)[blockIdx.x + 1];
-    if ((int)blockIdx.y * rows_each >= u.rows)
+    if ((int)blockIdx.y * kJoinRows<S, ROWS> >= u.rows)
         return;
-    const int lane = threadIdx.x & 31, parts = u.parts;
-    constexpr int kPer = S::DP / 32, kSide = 8;
+    constexpr int kLanes = S::DP / 4;
+    const int lane = threadIdx.x % kLanes, parts = u.parts;
+    const int row0 = blockIdx.y * kJoinRows<S, ROWS> + threadIdx.x / kLanes * ROWS;
     const float *first = part_of<S>(p, 2 * blockIdx.x + 1);  // the unit begins in this run
     const int64_t pitch = 2 * part_floats(S::kUnitRows, S::DP);
+    float top[ROWS], sum[ROWS];
+    float4 x[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        top[r] = -INFINITY;
+        sum[r] = 0.0f;
+        x[r] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
 #pragma unroll 1
-    for (int row = blockIdx.y * rows_each + (threadIdx.x >> 5);
-         row < min((int)(blockIdx.y + 1) * rows_each, u.rows); row += kJoinThreads / 32) {
-        float top = -INFINITY, sum = 0.0f, x[kPer];
+    for (int i0 = 0; i0 < parts; i0 += SIDE) {
+        float t[ROWS][SIDE], l[ROWS][SIDE];
+        float4 v[ROWS][SIDE];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            x[j] = 0.0f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < parts; i0 += kSide) {
-            float t[kSide], l[kSide], v[kSide][kPer];
+        for (int i = 0; i < SIDE; ++i) {
+            // Later parts lie in the slots of units begun before their run.
+            const float *from = first + (i0 + i) * pitch -
+                                (i0 + i > 0 ? part_floats(S::kUnitRows, S::DP) : 0);
 #pragma unroll
-            for (int i = 0; i < kSide; ++i) {
-                // Later parts lie in the slots of units begun before their run.
-                const float *from = first + (i0 + i) * pitch -
-                                    (i0 + i > 0 ? part_floats(S::kUnitRows, S::DP) : 0);
-                const bool is = i0 + i < parts;
-                t[i] = is ? from[row] : -INFINITY;
-                l[i] = is ? from[S::kUnitRows + row] : 0.0f;
-#pragma unroll
-                for (int j = 0; j < kPer; ++j)
-                    v[i][j] = is ? from[2 * S::kUnitRows + row * S::DP + lane * kPer + j] : 0.0f;
+            for (int r = 0; r < ROWS; ++r) {
+                const int row = row0 + r;
+                const bool is = i0 + i < parts && row < u.rows;
+                t[r][i] = is ? from[row] : -INFINITY;
+                l[r][i] = is ? from[S::kUnitRows + row] : 0.0f;
+                v[r][i] = is ? *reinterpret_cast<const float4 *>(from + 2 * S::kUnitRows + row * S::DP + lane * 4)
+                             : float4{0.0f, 0.0f, 0.0f, 0.0f};
             }
-            float most = top;
+        }
 #pragma unroll
-            for (int i = 0; i < kSide; ++i)
-                most = fmaxf(most, t[i]);
-            const float old = top == most ? 1.0f : exp2_fast(top - most);
-            sum *= old;
+        for (int r = 0; r < ROWS; ++r) {
+            float most = top[r];
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                x[j] *= old;
-            top = most;
+            for (int i = 0; i < SIDE; ++i)
+                most = fmaxf(most, t[r][i]);
+            const float old = top[r] == most ? 1.0f : exp2_fast(top[r] - most);
+            top[r] = most;
+            sum[r] *= old;
+            x[r].x *= old, x[r].y *= old, x[r].z *= old, x[r].w *= old;
 #pragma unroll
-            for (int i = 0; i < kSide; ++i)
+            for (int i = 0; i < SIDE; ++i)
                 if (i0 + i < parts) {
-                    const float f = t[i] == top ? 1.0f : exp2_fast(t[i] - top);
-                    sum = fmaf(l[i], f, sum);
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j)
-                        x[j] = fmaf(v[i][j], f, x[j]);
+                    const float f = t[r][i] == most ? 1.0f : exp2_fast(t[r][i] - most);
+                    sum[r] = fmaf(l[r][i], f, sum[r]);
+                    x[r].x = fmaf(v[r][i].x, f, x[r].x);
+                    x[r].y = fmaf(v[r][i].y, f, x[r].y);
+                    x[r].z = fmaf(v[r][i].z, f, x[r].z);
+                    x[r].w = fmaf(v[r][i].w, f, x[r].w);
                 }
         }
-        const int r = u.r0 + row, draft = r / p.group, q_head = u.head * p.group + r - draft * p.group;
-        const int64_t q_row = u.row0 + draft;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        uint32_t *out = reinterpret_cast<uint32_t *>(p.out + q_row * p.o_row + (int64_t)q_head * p.o_head);
-        if (lane * kPer < p.head_dim)
+    }
 #pragma unroll
-            for (int j = 0; j < kPer / 2; ++j)
-                out[lane * kPer / 2 + j] = pack16<S::BF16>(x[2 * j] * inv, x[2 * j + 1] * inv);
+    for (int k = 0; k < ROWS; ++k) {
+        if (row0 + k >= u.rows)
+            break;
+        const int r = u.r0 + row0 + k, draft = r / p.group, q_head = u.head * p.group + r - draft * p.group;
+        const int64_t q_row = u.row0 + draft;
+        const float inv = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+        if (lane * 4 < p.head_dim)
+            *reinterpret_cast<uint2 *>(p.out + q_row * p.o_row + (int64_t)q_head * p.o_head + lane * 8) =
+                uint2{pack16<S::BF16>(x[k].x * inv, x[k].y * inv), pack16<S::BF16>(x[k].z * inv, x[k].w * inv)};
         if (p.lse && lane == 0)
-            p.lse[q_row * p.q_heads + q_head] =
-                top == -INFINITY && sum == 0.0f ? -INFINITY : top * 0.69314718055994530942f + logf(sum);
+            p.lse[q_row * p.q_heads + q_head] = top[k] == -INFINITY && sum[k] == 0.0f
+                                                    ? -INFINITY
+                                                    : top[k] * 0.69314718055994530942f + logf(sum[k]);
     }
 }
 
@@ -1282,6 +1295,14 @@ cudaError_t launch_loads(const TreePlan &p, const Maps &maps, int ctas, bool pdl
     return launch(k_tree<S, BOXES>, dim3(ctas), S::kThreads, smem, pdl, stream, p, maps);
 }
 
+template <class S, int ROWS, int SIDE>
+cudaError_t launch_join(const TreePlan &p, int rows, int ctas, bool pdl, cudaStream_t stream)
+{
+    constexpr int each = kJoinRows<S, ROWS>;
+    return launch(k_tree_join<S, ROWS, SIDE>, dim3(ctas - 1, (rows + each - 1) / each), kJoinThreads, 0, pdl,
+                  stream, p, ctas);
+}
+
 template <class S>
 cudaError_t launch_shape(const TreePlan &p, int num_sms, bool pdl, cudaStream_t stream)
 {
@@ -1293,13 +1314,13 @@ cudaError_t launch_shape(const TreePlan &p, int num_sms, bool pdl, cudaStream_t 
     if (e != cudaSuccess || ctas < 2)
         return e;
     const int rows = p.rows < S::kUnitRows / p.group ? p.rows * p.group : S::kUnitRows;
-    // Units of many parts want many CTAs, a row a warp; of few parts, fewer CTAs,
-    // two rows a warp.  With 8 and 16 rows a CTA: 8 units on 304 runs of 131072
-    // positions 109 and 114 us, one chat 12.1 and 12.9; 256 units on 304 runs
-    // (32 chats) 68.3 and 67.1, 512 on 304 65.6 and 63.3, 8 on 152 82.7 and 82.5.
-    const int each = (int64_t)p.seqs * p.c.heads * 16 > ctas ? 16 : 8;
-    return launch(k_tree_join<S>, dim3(ctas - 1, (rows + each - 1) / each), kJoinThreads, 0, pdl, stream, p,
-                  ctas, each);
+    // Rows and parts at a time.  Few units have many parts and few rows in all:
+    // 1 and 8 (131072 positions, 128 rows 106 us; 1 and 16 107, 2 and 8 108; one
+    // chat 11.4, 12.0, 11.7).  Many units have two or three: 2 and 2, more rows in
+    // flight (32 chats 62.9 us; 1 and 8 66.3, 2 and 4 63.7, 4 and 4 69.0; 16
+    // sequences of 8192, 256 rows 142, 149, 143, 152).
+    const bool many = (int64_t)p.seqs * p.c.heads * 16 <= ctas;  // parts a unit
+    return many ? launch_join<S, 1, 8>(p, rows, ctas, pdl, stream) : launch_join<S, 2, 2>(p, rows, ctas, pdl, stream);
 }
 
 template <int DP, bool BF16>
