@@ -374,6 +374,18 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
     const int lane = threadIdx.x & 31, boxes = S::kPos / maps.box;
     uint32_t stage = 0, empty = 1;               // the next stage and the parity it waits for
     uint32_t k = 0, tail_use = 0, tail_parity = 0;  // loads; by stage: its last one, uses of kTail
+    // Waits (bounded) until the last loads of the stages have landed.  However
+    // the role ends: where another one's wait has run out, nobody else waits for
+    // them, and a CTA must not leave while they write its shared memory.
+    auto landed = [&]() {
+        for (uint32_t y = k - min(k, (uint32_t)S::kStages); y < k; ++y) {
+            const uint32_t s = y % S::kStages;
+            if (tail_use >> s & 1)
+                mbar_wait_bounded(cta.bar(kTail + s), (tail_parity >> s & 1) ^ 1);
+            else
+                mbar_wait_bounded(cta.bar(kFull + s), y / S::kStages & 1);
+        }
+    };
     Unit u;
     while (walk.next(u)) {
         // The table is read 32 boxes at a time, a lane each, one group ahead:
@@ -418,14 +430,7 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
                     }
                 }
                 if (!__all_sync(0xffffffffu, ok)) {
-                    // Let the tiles asked for land (bounded).
-                    for (uint32_t y = k - min(k, (uint32_t)S::kStages); y < k; ++y) {
-                        const uint32_t s = y % S::kStages;
-                        if (tail_use >> s & 1)
-                            mbar_wait_bounded(cta.bar(kTail + s), (tail_parity >> s & 1) ^ 1);
-                        else
-                            mbar_wait_bounded(cta.bar(kFull + s), y / S::kStages & 1);
-                    }
+                    landed();
                     return;
                 }
                 if (lane < boxes) {
@@ -453,6 +458,7 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
             first += kTile / maps.box;
         }
     }
+    landed();
 }
 
 // Looks over the values of the tiles that hold drafts.
@@ -1104,7 +1110,10 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
             }
         }
     }
-    // After an expired wait products may still run: let them end (bounded).
+    // After an expired wait products may still run: let them end (bounded).  Every
+    // role has ended by then, so that none sets the word later.
+    __syncwarp();
+    __syncthreads();
     if (threadIdx.x == 32 * (S::kSoftmaxWarps + 3) && cta.misc->abort) {
         umma_commit(cta.bar(kLast));
         mbar_wait_bounded(cta.bar(kLast), 0);

@@ -419,3 +419,27 @@ def test_expired_wait_is_reported_by_the_next_call(ctx):
             hasty.tree_attention(*c.args, **c.kw)
         assert e.value.code == tb.TB_ETIMEOUT
     Case(ctx, [3000], [4], seed=16).check()
+
+
+@pytest.mark.parametrize("lens,drafts,q_heads,dim", [([3000], [4], 4, 64), ([90], [7], 8, 128), ([700, 20, 5000], [40, 3, 60], 16, 128)])
+def test_calls_after_stopped_ones_are_right(ctx, lens, drafts, q_heads, dim):
+    """What a stopped call had asked for must have landed before it ends: the calls
+    behind it on the stream use the same shared memory.  Runs that fit the ring
+    (their loads are all asked for without a wait) and runs that do not."""
+    case = dict(q_heads=q_heads, heads=2, dim=dim, seed=24)
+    right = Case(ctx, lens, drafts, **case)
+    want, want_lse = (x.clone() for x in right.check())
+    with tb.Context(0, tb.options(kernel_wait_ns=0)) as hasty:
+        stopped = Case(hasty, lens, drafts, **case)
+        stopped.run()
+        for _ in range(30):
+            right.args[5].fill_(7.0)
+            right.kw["lse"].fill_(7.0)
+            try:
+                hasty.tree_attention(*stopped.args, **stopped.kw)
+            except tb.TBError as e:
+                assert e.code == tb.TB_ETIMEOUT
+            ctx.tree_attention(*right.args, **right.kw)
+            got, lse = right.args[5].clone(), right.kw["lse"].clone()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(lse, want_lse)
