@@ -111,7 +111,6 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
             if (lane >= d)
                 x += y;
         }
-        __syncthreads();
         if (lane == 31)
             found.sum[warp] = x;
         __syncthreads();
@@ -121,11 +120,16 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
     };
     Place r{};
     Seq s{};
-    int mine = 0, one = 0;
+    int mine = 0, one = 0, falls = 0;
     for (int b = threadIdx.x; b < p.seqs; b += THREADS) {
         s = seq_of(p, b, unit_rows);
         mine += one = work_of(p, s);
+        falls |= p.q_start[b] > p.q_start[b + 1];
     }
+    // Ascending sequences have no more rows than there are, which is what keeps
+    // the work in 32 bits; others are not dealt out at all.
+    if (__syncthreads_or(falls))
+        return r;
     int before = scan(mine, r.total);
     r.ctas = min(r.total, grid);
     if (c >= r.ctas)
@@ -142,6 +146,7 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
                 s = seq_of(p, b, unit_rows);
                 one = work_of(p, s);
             }
+            __syncthreads();  // found.sum has been read
             before = scan(one, sum);
         }
         if (r.at >= base + before && r.at - base - before < one) {

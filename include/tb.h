@@ -652,7 +652,8 @@ typedef struct {
     int32_t seqs;             /* sequences of this call, up to TB_TREE_MAX_SEQS */
     const int32_t *seq_slots; /* device [seqs]: the slot of each; NULL = 0, 1, 2, ... */
     const int32_t *q_start;   /* device [seqs + 1]: query rows of sequence b are
-                                 q_start[b] .. q_start[b + 1] - 1, ascending from 0 */
+                                 q_start[b] .. q_start[b + 1] - 1, ascending from 0
+                                 (where it descends, nothing is computed) */
     int32_t rows;             /* query rows in all, q_start[seqs] */
     int32_t q_heads;          /* a multiple of kv_heads; head h reads cache head
                                  h / (q_heads / kv_heads) */

@@ -443,3 +443,24 @@ def test_calls_after_stopped_ones_are_right(ctx, lens, drafts, q_heads, dim):
             got, lse = right.args[5].clone(), right.kw["lse"].clone()
             torch.cuda.synchronize()
             assert torch.equal(got, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("seqs", [3, 700])
+def test_query_rows_that_do_not_ascend_are_left_alone(ctx, seqs):
+    """Sequences that name rows again could make more work than the call's counts
+    hold: nothing is computed then."""
+    c = Case(ctx, [40] * seqs, [2] * seqs, seed=25)
+    c.run()
+    cache, layer, q, q_start, mask, out, work = c.args
+    for at, value in ((1, 2 * seqs), (seqs, 0), (seqs - 1, -5)):
+        bad = q_start.clone()
+        bad[at] = value
+        out.fill_(7.0)
+        c.kw["lse"].fill_(7.0)
+        ctx.tree_attention(cache, layer, q, bad, mask, out, work, **c.kw)
+        torch.cuda.synchronize()
+        assert bool((out == 7.0).all()) and bool((c.kw["lse"] == 7.0).all())
+    ctx.tree_attention(*c.args, **c.kw)
+    torch.cuda.synchronize()
+    c.rows = None if seqs < 10 else list(range(0, 2 * seqs, 97))
+    c.compare(out, c.kw["lse"])
