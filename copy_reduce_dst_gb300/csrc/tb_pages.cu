@@ -179,6 +179,7 @@ __device__ __forceinline__ uint32_t cluster_size()
 // All threads of the cluster; orders their memory accesses before and after.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();  // the barrier is one for whole warps
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -819,6 +819,7 @@ __device__ __forceinline__ void write_unit(const TreePlan &p, const Cta &cta, co
 #pragma unroll 1
     for (int g = 0; g < S::DP / 32; ++g) {
         uint32_t o[32];
+        __syncwarp();  // rows part ways below; tensor memory is read by whole warps
         tmem_load32(o, sum_cols + 32 * g);
         tmem_wait_load(o);
         if (!real)
@@ -1004,7 +1005,8 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                     top = here;
                     sum *= old;
                 }
-                if (j != u.j0 && __any_sync(0xffffffffu, moves)) {
+                const bool any = __any_sync(0xffffffffu, moves);  // brings the lanes together too
+                if (j != u.j0 && any) {
 #pragma unroll 1
                     for (int g = 0; g < S::DP / 16; ++g) {
                         uint32_t o[16];
@@ -1091,6 +1093,7 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
     const Walk walk(p, S::kUnitRows, place, runs ? place.start(blockIdx.x + 1) - place.at : 0);
     if (threadIdx.x == 32 * (S::kSoftmaxWarps + 2))
         note_cut<S>(p, place, walk);
+    __syncwarp();  // the register instructions below are for whole warps
     if (runs) {
         // Registers a thread: launched with 168 (two streams) or 128; what the
         // last four warps give up is what the softmax warps take.
