@@ -94,7 +94,7 @@ struct Place {
 
 // Shared memory of find_run.
 struct Found {
-    int sum[32], b, off;
+    int sum[32], b, off, falls;
     Seq s;
 };
 
@@ -111,6 +111,7 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
             if (lane >= d)
                 x += y;
         }
+        __syncthreads();
         if (lane == 31)
             found.sum[warp] = x;
         __syncthreads();
@@ -120,16 +121,11 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
     };
     Place r{};
     Seq s{};
-    int mine = 0, one = 0, falls = 0;
+    int mine = 0, one = 0;
     for (int b = threadIdx.x; b < p.seqs; b += THREADS) {
         s = seq_of(p, b, unit_rows);
         mine += one = work_of(p, s);
-        falls |= p.q_start[b] > p.q_start[b + 1];
     }
-    // Ascending sequences have no more rows than there are, which is what keeps
-    // the work in 32 bits; others are not dealt out at all.
-    if (__syncthreads_or(falls))
-        return r;
     int before = scan(mine, r.total);
     r.ctas = min(r.total, grid);
     if (c >= r.ctas)
@@ -146,7 +142,6 @@ __device__ Place find_run(const TreePlan &p, int unit_rows, int grid, int c, Fou
                 s = seq_of(p, b, unit_rows);
                 one = work_of(p, s);
             }
-            __syncthreads();  // found.sum has been read
             before = scan(one, sum);
         }
         if (r.at >= base + before && r.at - base - before < one) {
@@ -1085,10 +1080,24 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
         tmem_alloc<S::kCols>(smem_u32(&cta.misc->tmem));
     pdl_wait_prerequisite();
     pdl_launch_dependents();
-    const Place place = find_run<S::kThreads>(p, S::kUnitRows, gridDim.x, blockIdx.x, cta.misc->found);
+    // Ascending sequences have no more rows than there are, which is what keeps
+    // the work in 32 bits; others are not dealt out at all.  A warp of its own
+    // looks: in the loop of find_run it made the kernel's code 4% slower.
+    if (warp == S::kSoftmaxWarps + 1) {
+        int falls = 0;
+#pragma unroll 4
+        for (int b = lane; b < p.seqs; b += 32)
+            falls |= p.q_start[b] > p.q_start[b + 1];
+        falls = __any_sync(0xffffffffu, falls);
+        if (lane == 0)
+            cta.misc->found.falls = falls;
+    }
+    Place place = find_run<S::kThreads>(p, S::kUnitRows, gridDim.x, blockIdx.x, cta.misc->found);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (cta.misc->found.falls)
+        place.ctas = 0;
     const bool runs = (int)blockIdx.x < place.ctas;
     const Walk walk(p, S::kUnitRows, place, runs ? place.start(blockIdx.x + 1) - place.at : 0);
     if (threadIdx.x == 32 * (S::kSoftmaxWarps + 2))
@@ -1118,17 +1127,20 @@ __global__ void __launch_bounds__(S::kThreads, 3 - S::STREAMS)
             }
         }
     }
-    // After an expired wait products may still run: let them end (bounded).  Every
-    // role has ended by then, so that none sets the word later.
-    __syncwarp();
-    __syncthreads();
-    if (threadIdx.x == 32 * (S::kSoftmaxWarps + 3) && cta.misc->abort) {
-        umma_commit(cta.bar(kLast));
-        mbar_wait_bounded(cta.bar(kLast), 0);
-    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // After an expired wait products may still run: let them end (bounded).  Every
+    // role has ended by now, so that none sets the word later.
+    if (cta.misc->abort) {
+        if (threadIdx.x == 32 * (S::kSoftmaxWarps + 3)) {
+            umma_commit(cta.bar(kLast));
+            mbar_wait_bounded(cta.bar(kLast), 0);
+        }
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == S::kSoftmaxWarps) {
         tc_fence_after();
         tmem_free<S::kCols>(cta.misc->tmem);
