@@ -394,7 +394,7 @@ __device__ void box_role(const TreePlan &p, const Maps &maps, const Cta &cta, Wa
         auto look_up = [&](int group, int &page, int &token) {
             const int pos = (32 * group + lane) * maps.box, at = pos / c.page_tokens;
             token = pos - at * c.page_tokens;
-            page = pos < u.s.end && at < c.width ? __ldg(row + at) : -1;
+            page = pos < u.s.end && at < c.width ? row[at] : -1;
         };
         int first = u.j0 * (kTile / maps.box);  // the stage's first box
         int group = first / 32, page, token, next_page, next_token;
@@ -765,12 +765,12 @@ struct MaskRow {
     __device__ MaskRow(const TreePlan &p, const Seq &s, int64_t row)
         : words(p.mask + row * p.mask_words), count(p.mask_words), T(s.end > 0 ? s.T : 0)
     {
-        first = count > 0 ? __ldg(words) : 0;
-        second = count > 1 ? __ldg(words + 1) : 0;
+        first = count > 0 ? words[0] : 0;
+        second = count > 1 ? words[1] : 0;
     }
     __device__ uint32_t word(int w) const
     {
-        return w == 0 ? first : w == 1 ? second : w < count ? __ldg(words + w) : 0;
+        return w == 0 ? first : w == 1 ? second : w < count ? words[w] : 0;
     }
     // Bits for 32 positions from draft d (negative: committed positions, seen)
     // on; drafts from T on are not seen.
@@ -916,8 +916,8 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
             for (int i = 0; i < kChunks; ++i) {
                 q[i] = uint4{0, 0, 0, 0};
                 if (row + i * step < u.rows && tid % kChunks * 16 < p.c.row_bytes)
-                    q[i] = __ldg(reinterpret_cast<const uint4 *>(
-                        from + (int64_t)(u.s.row0 + draft) * p.q_row + (int64_t)h * p.q_head));
+                    q[i] = *reinterpret_cast<const uint4 *>(
+                        from + (int64_t)(u.s.row0 + draft) * p.q_row + (int64_t)h * p.q_head);
                 draft += d_step;
                 h += h_step;
                 if (h >= p.group) {
