@@ -711,6 +711,18 @@ __device__ void product_role(const TreePlan &p, const Cta &cta, Walk walk)
 // ---------------------------------------------------------------------------
 // Softmax: a thread is a row of its stream's row tile.
 // ---------------------------------------------------------------------------
+// Weights of f16 are 2^7 times exp(s - m).  The running maximum may lag by 2^8, so
+// they stay at or below 2^15, inside the type; what a long context's many small
+// ones add up to is kept: 16 bits hold weights down to 2^-21 of the largest in
+// full and others to within 2^-32 of it (2^-14 and 2^-25 without: 131072
+// positions, 17 below one in the exponent, moved the output by 2e-3 of their value).  Sums
+// and outputs grow alike, which leaves the quotient; the logarithm takes the
+// sums back.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
+template <bool BF16>
+constexpr float kUnlift = BF16 ? 1.0f : 0.0078125f;
+
 // Partial sums of a cut unit: [slot][row] maxima (of scores times scale *
 // log2 e), sums and, unnormalised, outputs.  Run c writes the unit it begins
 // inside of to slot 2 c and one that goes on after it to slot 2 c + 1.
@@ -808,7 +820,7 @@ __device__ __forceinline__ void write_unit(const TreePlan &p, const Cta &cta, co
             part[S::kUnitRows + mine] = sum;
         } else if (p.lse) {
             p.lse[q_row * p.q_heads + q_head] =
-                top == -INFINITY && sum == 0.0f ? -INFINITY : top * fabsf(p.scale) + logf(sum);
+                top == -INFINITY && sum == 0.0f ? -INFINITY : top * fabsf(p.scale) + logf(sum * kUnlift<S::BF16>);
         }
     }
 #pragma unroll 1
@@ -1013,11 +1025,12 @@ __device__ void softmax_role(const TreePlan &p, const Cta &cta, Walk walk, int r
                         tmem_store16(sum_cols + 16 * g, o);
                     }
                 }
-                const float shift = top == -INFINITY ? 0.0f : top * c;
+                const float shift = top == -INFINITY ? 0.0f : fmaf(top, c, -kLift<S::BF16>);
                 float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 // Weights in 16 bits for the second product, as its operand
-                // type asks: a relative error of at most half an ulp each; the
-                // sum is of the unrounded ones.
+                // type asks: a relative error of at most half an ulp each, for
+                // f16 down to 2^-21 of the largest; the sum is of the unrounded
+                // ones.
 #pragma unroll 1
                 for (int g = 0; g < 4; ++g) {
                     uint32_t w[16];
@@ -1233,7 +1246,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_tree_join(const TreePlan p, in
         if (p.lse && lane == 0)
             p.lse[q_row * p.q_heads + q_head] = top[k] == -INFINITY && sum[k] == 0.0f
                                                     ? -INFINITY
-                                                    : top[k] * 0.69314718055994530942f + logf(sum[k]);
+                                                    : top[k] * 0.69314718055994530942f + logf(sum[k] * kUnlift<S::BF16>);
     }
 }
 

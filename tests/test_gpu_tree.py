@@ -464,3 +464,44 @@ def test_query_rows_that_do_not_ascend_are_left_alone(ctx, seqs):
     torch.cuda.synchronize()
     c.rows = None if seqs < 10 else list(range(0, 2 * seqs, 97))
     c.compare(out, c.kw["lse"])
+
+
+@pytest.mark.parametrize("below", [9.0, 14.0, 16.5, 17.0, 17.5, 18.0, 20.0])
+@pytest.mark.parametrize("lens", [[2000] * 320, [131072, 17, 900]])
+def test_many_small_weights_of_f16_add_up(ctx, below, lens):
+    """One position leads all others by `below` in the exponent: their weights are far
+    below f16's 2^-14, their sum is not.  16-bit weights 2^7 times exp(s - m) are off by
+    2^-11 of each or, below 2^-21, by 2^-32 each; the whole result by those and its
+    own rounding."""
+    c = Case(ctx, lens, [1] * len(lens), q_heads=1, heads=1, dim=64, P=64, dtype="f16", seed=26,
+             check_rows=3)
+    g = torch.Generator().manual_seed(27)
+    k, v = c.pools
+    k.zero_()
+    v.copy_(torch.rand(v.shape, generator=g) + 0.5)
+    c.q.fill_(1.0)
+    c.scale, c.rows = 0.125, [0, 1, len(lens) - 1]
+    leaders = [(b, n // 3) for b, n in enumerate(lens)]
+    for b, j in leaders:
+        k[0, c.table[b, j // c.P], j % c.P] = below / 8.0  # 64 products of one: exact
+        v[0, c.table[b, j // c.P], j % c.P] = 0.0
+    out, lse = c.run()
+    want, want_lse, reach, logit = (x[c.rows] for x in c.want())
+    u, slack = 2.0**-11, (64 + 8) * 2.0**-24 * logit + 2.0**-20
+    tail = u * reach + np.array([lens[i] for i in c.rows])[:, None, None] * 2.0**-32 * float(v.max())
+    bound = u * want * 1.01 + (tail + 2 * slack[..., None] * reach) * (1 + u) + 2.0**-25
+    off = np.abs(out.float().cpu().numpy().astype(np.float64)[c.rows] - want)
+    assert np.all(off <= bound), float((off / bound).max())
+    assert np.all(np.abs(lse.cpu().numpy()[c.rows] - want_lse) <= slack + 2.0**-20 * (1 + np.abs(want_lse)))
+
+
+def test_infinite_values_under_small_f16_weights(ctx):
+    c = Case(ctx, [300], [2], q_heads=1, heads=1, dim=64, dtype="f16", seed=28)
+    k, v = c.pools
+    k.zero_()
+    c.q.fill_(1.0)
+    c.scale = 0.125
+    k[0, c.table[0, 1], 3] = 2.25  # 18 above the others
+    v[0, c.table[0, 0], 5, :, 7] = float("inf")
+    out, _ = c.run()
+    assert torch.isposinf(out[:, :, 7]).all() and torch.isfinite(out[:, :, 8:]).all()
