@@ -110,6 +110,37 @@ int view_of(tb_ctx *ctx, const tb_kv_cache *cache, bool pools, bool table, const
     return TB_OK;
 }
 
+// Whether an element of the one pool lies on one of the other: whether some
+// difference of two rows' places is within a row of the pools' distance.  As
+// the strides are nested (view_of), the largest one's multiple has to be the
+// one below or above what is left, and so on down.
+bool pools_meet(const tb::KvView &v)
+{
+    std::pair<int64_t, int64_t> dim[4] = {{v.layer_stride, v.layers},
+                                          {v.page_stride, v.pages},
+                                          {v.token_stride, v.page_tokens},
+                                          {v.head_stride, v.heads}};
+    std::sort(dim, dim + 4);
+    int64_t left[16] = {(int64_t)((uintptr_t)v.pool[1] - (uintptr_t)v.pool[0])};
+    int n = 1;
+    for (int d = 3; d >= 0; --d) {
+        if (dim[d].second == 1)
+            continue;
+        for (int i = n - 1; i >= 0; --i) {
+            const int64_t stride = dim[d].first, most = dim[d].second - 1;
+            int64_t low = left[i] / stride;
+            if (low * stride > left[i])
+                --low;
+            const int64_t a = std::min(std::max(low, -most), most);
+            const int64_t b = std::min(std::max(low + 1, -most), most);
+            left[i] -= a * stride;
+            left[n + i] = left[i] + (a - b) * stride;
+        }
+        n *= 2;
+    }
+    return std::any_of(left, left + n, [&](int64_t x) { return x > -v.row_bytes && x < v.row_bytes; });
+}
+
 // Whether two arrays of n words share none.
 bool apart(const int32_t *a, const int32_t *b, uint64_t n)
 {
@@ -203,6 +234,8 @@ int tb_kv_compact(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *start, c
     if (!start || !count || !status || keep_stride < 0 || (keep_stride > 0 && !keep))
         return fail(ctx, TB_EINVAL,
                     "kv_compact: null start, keep, count or status, or keep_stride < 0");
+    if (pools_meet(v))
+        return fail(ctx, TB_EINVAL, "kv_compact: the two pools share an element");
     if (!apart(start, v.lens, (uint64_t)v.slots) || !apart(count, v.lens, (uint64_t)v.slots))
         return fail(ctx, TB_EINVAL, "kv_compact: start or count overlaps the cache's lens");
     if (v.slots > 65535)

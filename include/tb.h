@@ -580,7 +580,9 @@ typedef struct {
        Pointers, strides and head_dim * element size are multiples of 16.  Any
        order of the four strided dimensions is fine as long as no two elements
        share an address: tokens before heads, heads before tokens, keys and
-       values interleaved. */
+       values interleaved.  k and v may be one pool (the same pointer) where
+       keys and values are the same, except for tb_kv_compact: describe the two
+       halves of its rows as k and v there. */
     void *k, *v;
     int32_t *table;           /* device [slots][table_width] */
     int32_t *held;            /* device [slots]: pages the slot holds */
@@ -638,7 +640,9 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
    keep = the accepted path of a draft tree this commits that path; with start
    = 0 it drops the tokens not listed.  Pages past the new length stay with
    the slot (tb_kv_resize gives them back).  A negative count leaves its slot
-   alone.  status[s] (device [slots]) receives 0; 1 when a token would move
+   alone.  Pools that share an element are refused: a token's place is written
+   while others are read, once for each pool.  status[s] (device [slots])
+   receives 0; 1 when a token would move
    into a page that other rows share; 2 when the list does not ascend, count
    exceeds keep_stride or a position lies outside the slot's pages; a slot
    with a nonzero status is unchanged. */

@@ -403,3 +403,32 @@ def test_refusals(ctx):
     with pytest.raises(ValueError):
         tb.kv_cache(x.pools[0], None)
     x.check()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("shift", ["same", "token", "head", "page", "layer", "part of a row", "backwards"])
+def test_compact_refuses_pools_that_share_memory(ctx, layout, shift):
+    """One pool for both would have its tokens moved twice, the second time from
+    places already written."""
+    x = Cache(slots=2, width=4, pages=10, P=4, heads=3, dim=32, layers=2, layout=layout)
+    s, many = x.c.struct, dev(np.zeros(2, np.int32))
+    s.v = s.k + {"same": 0, "token": s.token_stride, "head": s.head_stride, "page": 7 * s.page_stride,
+                 "layer": s.layer_stride, "part of a row": 2 * s.head_stride + 16,
+                 "backwards": -3 * s.page_stride - 2 * s.token_stride - 48}[shift]
+    refused(tb.TB_EINVAL, ctx.kv_compact, x.c, many, many[:, None].contiguous(), many, torch.empty_like(many))
+
+
+def test_compact_of_the_two_halves_of_a_pools_rows(ctx):
+    """One pool with rows of 48 elements described as keys of 16 and values of 16,
+    with a gap between them: nothing is shared."""
+    x = Cache(slots=2, width=4, pages=10, P=4, heads=3, dim=16, layers=2)
+    whole = torch.zeros(2, 10, 4, 3, 48, dtype=torch.bfloat16, device="cuda")
+    for pool, at in zip(x.pools, (32, 0)):
+        whole[..., at:at + 16] = pool
+    x.pools = [whole[..., 32:], whole[..., :16]]
+    x.describe()
+    x.resize(ctx, [16, 16])
+    x.set_lens([16, 11])
+    x.compact(ctx, [3, 0], [[0, 2, 5, 6], [1, 2, 3, 9]], [4, 4])
+    x.check()
+    assert int((whole[..., 16:32] != 0).sum()) == 0
