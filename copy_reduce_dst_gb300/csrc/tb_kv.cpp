@@ -6,6 +6,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <utility>
 
 #include "tb_internal.h"
@@ -141,11 +142,22 @@ bool pools_meet(const tb::KvView &v)
     return std::any_of(left, left + n, [&](int64_t x) { return x > -v.row_bytes && x < v.row_bytes; });
 }
 
-// Whether two arrays of n words share none.
-bool apart(const int32_t *a, const int32_t *b, uint64_t n)
+// An array of 32-bit words.
+struct Words {
+    const int32_t *at;
+    uint64_t n;
+};
+
+// Whether two arrays share no word (an empty one shares none).
+bool apart(const Words &a, const Words &b)
 {
-    return reinterpret_cast<uintptr_t>(a) + 4 * n <= reinterpret_cast<uintptr_t>(b) ||
-           reinterpret_cast<uintptr_t>(b) + 4 * n <= reinterpret_cast<uintptr_t>(a);
+    return !a.n || !b.n || reinterpret_cast<uintptr_t>(a.at) + 4 * a.n <= reinterpret_cast<uintptr_t>(b.at) ||
+           reinterpret_cast<uintptr_t>(b.at) + 4 * b.n <= reinterpret_cast<uintptr_t>(a.at);
+}
+
+bool apart(const Words &a, std::initializer_list<Words> others)
+{
+    return std::all_of(others.begin(), others.end(), [&](const Words &b) { return apart(a, b); });
 }
 
 int launched(tb_ctx *ctx, cudaError_t e, const char *what)
@@ -190,6 +202,13 @@ int tb_kv_resize(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *capacity,
         return fail(ctx, TB_EINVAL, "kv_resize: null capacity or status");
     if (v.slots > TB_KV_MAX_SLOTS)
         return fail(ctx, TB_ENOTSUP, "kv_resize: more than %d slots", TB_KV_MAX_SLOTS);
+    const uint64_t slots = (uint64_t)v.slots;
+    const Words table{v.table, slots * (uint64_t)v.width}, held{v.held, slots}, lens{v.lens, slots},
+        refs{v.refs, (uint64_t)v.pages}, caps{capacity, slots};
+    // (Capacities that are the lengths themselves stay what they are.)
+    if (!apart(caps, {table, held, refs}) || !apart(Words{status, 1}, {table, held, lens, refs, caps}))
+        return fail(ctx, TB_EINVAL, "kv_resize: capacity or status overlaps what the call changes, or "
+                                    "status overlaps capacity");
     tb::DeviceScope scope(tb::ctx_device(ctx));
     return launched(ctx,
                     tb::launch_kv_resize(v, capacity, status, tb::ctx_options(ctx).use_pdl != 0,
@@ -210,10 +229,19 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents, in
         return fail(ctx, TB_EINVAL, "kv_fork: null parents, output or status");
     if (v.slots > TB_KV_MAX_SLOTS)
         return fail(ctx, TB_ENOTSUP, "kv_fork: more than %d slots", TB_KV_MAX_SLOTS);
-    const uint64_t rows = (uint64_t)v.slots * (uint64_t)v.width;
-    if (!apart(table_out, v.table, rows) || !apart(held_out, v.held, (uint64_t)v.slots) ||
-        !apart(lens_out, v.lens, (uint64_t)v.slots))
-        return fail(ctx, TB_EINVAL, "kv_fork: an output overlaps the array it replaces");
+    const uint64_t slots = (uint64_t)v.slots, rows = slots * (uint64_t)v.width;
+    const Words table{v.table, rows}, held{v.held, slots}, lens{v.lens, slots}, refs{v.refs, (uint64_t)v.pages},
+        list{parents, slots};
+    const Words outs[] = {{table_out, rows}, {held_out, slots}, {lens_out, slots}, {status, 1}};
+    for (int i = 0; i < 4; ++i) {
+        bool fine = apart(outs[i], {table, held, lens, refs, list});
+        for (int j = 0; j < i; ++j)
+            fine = fine && apart(outs[i], outs[j]);
+        if (!fine)
+            return fail(ctx, TB_EINVAL, "kv_fork: an output or status overlaps an input or another output");
+    }
+    if (!apart(refs, list))
+        return fail(ctx, TB_EINVAL, "kv_fork: parents overlaps refs");
     tb::DeviceScope scope(tb::ctx_device(ctx));
     return launched(ctx,
                     tb::launch_kv_fork(v, parents, table_out, held_out, lens_out, status,
@@ -236,8 +264,14 @@ int tb_kv_compact(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *start, c
                     "kv_compact: null start, keep, count or status, or keep_stride < 0");
     if (pools_meet(v))
         return fail(ctx, TB_EINVAL, "kv_compact: the two pools share an element");
-    if (!apart(start, v.lens, (uint64_t)v.slots) || !apart(count, v.lens, (uint64_t)v.slots))
-        return fail(ctx, TB_EINVAL, "kv_compact: start or count overlaps the cache's lens");
+    const uint64_t slots = (uint64_t)v.slots;
+    const Words table{v.table, slots * (uint64_t)v.width}, held{v.held, slots}, lens{v.lens, slots},
+        refs{v.refs, (uint64_t)v.pages}, from{start, slots}, kept{keep, slots * (uint64_t)keep_stride},
+        counts{count, slots};
+    if (!apart(lens, {from, kept, counts}))
+        return fail(ctx, TB_EINVAL, "kv_compact: start, keep or count overlaps the cache's lens");
+    if (!apart(Words{status, slots}, {table, held, lens, refs, from, kept, counts}))
+        return fail(ctx, TB_EINVAL, "kv_compact: status overlaps an input or the cache's arrays");
     if (v.slots > 65535)
         return fail(ctx, TB_ENOTSUP, "kv_compact: more than 65535 slots");
     tb::DeviceScope scope(tb::ctx_device(ctx));

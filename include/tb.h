@@ -554,7 +554,9 @@ int tb_copy_each(tb_ctx *ctx, const tb_copy_desc *desc, size_t n, tb_stream stre
    a count of the table entries that name each page.  Every call below is
    asynchronous on `stream`, reads its lists from device memory (so no list
    goes through the host), allocates nothing, and may be captured into a CUDA
-   graph.  Calls that change the table or the counts are to be ordered with
+   graph.  An array that a call writes must share no word with one that it reads
+   or another that it writes (TB_EINVAL), except the cache's own and the
+   capacities of a resize, which may be the lengths themselves.  Calls that change the table or the counts are to be ordered with
    one another (one stream, or events).  A page number or a position outside
    the cache is never dereferenced.
 
@@ -618,8 +620,8 @@ int tb_kv_resize(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *capacity,
 /* Replaces every slot s by the sequence of slot parents[s] (device [slots];
    negative: the slot becomes empty, s: it goes on), as a step of a beam search
    does, without copying full pages.  The new table, held and lens go to the
-   three output arrays (the same shapes, not overlapping cache->table, held,
-   lens; the next call's inputs), the counts and pages change in place.
+   three output arrays (the same shapes, the next call's inputs), the counts
+   and pages change in place.
    A parent's full pages are shared by all its children.  Its last page, if
    partly filled, and its pages after that go to one child: the slot itself if
    it goes on, else the lowest one; each other child takes a fresh page (in
@@ -635,7 +637,7 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
 /* Squeezes kept tokens together: in slot s, for i in [0, count[s]), the token
    at start[s] + keep[s * keep_stride + i] moves to start[s] + i, in every
    layer, keys and values, as if in order of i; then lens[s] = start[s] +
-   count[s].  keep ascends strictly; start and count must not overlap lens.
+   count[s].  keep ascends strictly.
    With start = the committed length and
    keep = the accepted path of a draft tree this commits that path; with start
    = 0 it drops the tokens not listed.  Pages past the new length stay with

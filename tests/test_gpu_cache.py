@@ -432,3 +432,46 @@ def test_compact_of_the_two_halves_of_a_pools_rows(ctx):
     x.compact(ctx, [3, 0], [[0, 2, 5, 6], [1, 2, 3, 9]], [4, 4])
     x.check()
     assert int((whole[..., 16:32] != 0).sum()) == 0
+
+
+def test_arrays_that_overlap_are_refused(ctx):
+    """What a call writes must not be what it reads, or another thing that it writes."""
+    x = Cache(slots=3, width=4, pages=12, P=4)
+    x.resize(ctx, [9, 5, 0])
+    x.set_lens([9, 4, 0])
+    x.check(0)
+    ints = dev(np.zeros(64, np.int32))
+    three, one, table = (lambda i: ints[i:i + 3]), x.status, ints[32:44].view(3, 4)
+    s = x.c.struct
+    # resize: capacity and status against what changes, status against capacity
+    for capacity in (x.held, x.refs[2:5], x.table[1, :3]):
+        refused(tb.TB_EINVAL, ctx.kv_resize, x.c, capacity, one)
+    for status in (x.held[2:], x.lens[:1], x.refs[11:], x.table[2, 3:]):
+        refused(tb.TB_EINVAL, ctx.kv_resize, x.c, three(0), status)
+    refused(tb.TB_EINVAL, ctx.kv_resize, x.c, three(0), ints[2:3])
+    # fork: each output against each input and the other outputs
+    good = dict(parents=three(0), table_out=table, held_out=three(4), lens_out=three(8), status=ints[12:13])
+    for name, value in (("table_out", x.refs.view(3, 4)), ("table_out", ints[6:18].view(3, 4)), ("held_out", x.lens),
+                        ("held_out", three(1)), ("held_out", x.table[0, 1:]), ("lens_out", x.held),
+                        ("lens_out", three(5)), ("lens_out", x.refs[:3]), ("status", ints[2:3]), ("status", x.lens[2:]),
+                        ("status", ints[10:11]), ("status", ints[40:41]), ("parents", x.refs[9:])):
+        refused(tb.TB_EINVAL, ctx.kv_fork, x.c, **{**good, name: value})
+    # compact: status against everything, keep against lens
+    keep = ints[32:38].view(3, 2)
+    good = dict(start=three(0), keep=keep, count=three(4), status=three(8))
+    for name, value in (("status", three(1)), ("status", three(5)), ("status", ints[37:40]), ("status", x.lens),
+                        ("status", x.held), ("status", x.refs[4:7]), ("keep", x.lens.view(3, 1)), ("start", x.lens)):
+        refused(tb.TB_EINVAL, ctx.kv_compact, x.c, **{**good, name: value})
+    x.check(0)
+    # neighbours are fine, and so are the lengths as capacities
+    ctx.kv_resize(x.c, x.lens, ints[3:4])
+    assert x.model.resize([9, 4, 0]) == 0
+    x.check()
+    ints[:3] = torch.tensor([0, 1, -1])
+    out = (ints[3:15].view(3, 4), ints[15:18], ints[18:21])
+    ctx.kv_fork(x.c, ints[:3], *out, ints[21:22])
+    x.table, x.held, x.lens = out
+    x.describe()
+    assert x.model.fork([0, 1, -1]) == 0
+    x.check()
+    assert int(ints[21]) == 0
