@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as ct
 import os
+import sys
 from dataclasses import dataclass
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libtb.so")
@@ -634,6 +635,14 @@ class Context:
         return {name: getattr(s, name) for name, _ in BatchStats._fields_}
 
     # -- paged key/value cache ---------------------------------------------
+    # Their lists are tensors, often ones made a line before: without a stream
+    # the calls run on PyTorch's current one, behind what made the tensors, and
+    # memory that a dropped tensor gives back is written only after they have read it.
+    def _stream(self, stream) -> int:
+        if stream is None and "torch" in sys.modules:
+            return sys.modules["torch"].cuda.current_stream(self.device).cuda_stream
+        return stream_handle(stream)
+
     def kv_copy_pages(self, cache: KvCache, src, dst, n: int | None = None, tokens=None,
                       stream=None):
         """tb_kv_copy_pages: page src[i] to page dst[i] in every layer, keys
@@ -647,13 +656,13 @@ class Context:
             n = most
         elif n > most:
             raise ValueError(f"n is {n}, the shortest list has {most} entries")
-        self._ok(lib.tb_kv_copy_pages(self._h, cache.ref, s, d, m, n, stream_handle(stream)),
+        self._ok(lib.tb_kv_copy_pages(self._h, cache.ref, s, d, m, n, self._stream(stream)),
                  "tb_kv_copy_pages")
 
     def kv_resize(self, cache: KvCache, capacity, status, stream=None):
         """tb_kv_resize: each slot gets exactly the pages of capacity[s] tokens."""
         self._ok(lib.tb_kv_resize(self._h, cache.ref, _int32(capacity, "capacity", cache.per_slot),
-                                  _int32(status, "status", (1,)), stream_handle(stream)),
+                                  _int32(status, "status", (1,)), self._stream(stream)),
                  "tb_kv_resize")
 
     def kv_fork(self, cache: KvCache, parents, table_out, held_out, lens_out, status, stream=None):
@@ -663,7 +672,7 @@ class Context:
                                 _int32(table_out, "table_out", cache.table_shape),
                                 _int32(held_out, "held_out", slots),
                                 _int32(lens_out, "lens_out", slots),
-                                _int32(status, "status", (1,)), stream_handle(stream)),
+                                _int32(status, "status", (1,)), self._stream(stream)),
                  "tb_kv_fork")
 
     def kv_compact(self, cache: KvCache, start, keep, count, status, stream=None):
@@ -672,7 +681,7 @@ class Context:
         self._ok(lib.tb_kv_compact(self._h, cache.ref, _int32(start, "start", slots),
                                    _int32(keep, "keep", slots + (width,)), width,
                                    _int32(count, "count", slots), _int32(status, "status", slots),
-                                   stream_handle(stream)), "tb_kv_compact")
+                                   self._stream(stream)), "tb_kv_compact")
 
     def tree_attention_workspace(self, cache: KvCache, q_heads: int) -> int:
         """Bytes of workspace tree_attention needs (tb_tree_attention_workspace)."""
@@ -710,7 +719,7 @@ class Context:
                  q_row * e, q_head * e, o_row * e, o_head * e,
                  0 if lse is None else lse.data_ptr(), bits, words, workspace.data_ptr(),
                  workspace.numel() * workspace.element_size())
-        self._ok(lib.tb_tree_attention(self._h, ct.byref(t), stream_handle(stream)),
+        self._ok(lib.tb_tree_attention(self._h, ct.byref(t), self._stream(stream)),
                  "tb_tree_attention")
 
     # -- validation --------------------------------------------------------

@@ -475,3 +475,43 @@ def test_arrays_that_overlap_are_refused(ctx):
     assert x.model.fork([0, 1, -1]) == 0
     x.check()
     assert int(ints[21]) == 0
+
+
+def test_calls_run_on_the_current_stream(ctx):
+    """Without stream= a call runs behind what the current stream still has to do,
+    and is captured where that stream is."""
+    x = Cache(slots=3, width=6, pages=20, P=4)
+    busy, stream = torch.randn(8192, 8192, device="cuda").bfloat16(), torch.cuda.Stream()
+    late = dev(np.array([9, 5, 22], np.int32))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        for _ in range(40):
+            busy @ busy
+        ctx.kv_resize(x.c, late + 1, x.status)  # made behind the products, dropped at once
+        reuse = torch.full((3,), 1, dtype=torch.int32, device="cuda")
+        for _ in range(10):
+            busy @ busy
+        x.lens.copy_(late)
+        out = [torch.full_like(t, 77) for t in (x.table, x.held, x.lens)]
+        ctx.kv_fork(x.c, reuse - 1, *out, x.status)
+    torch.cuda.synchronize()
+    assert x.model.resize([10, 6, 23]) == 0
+    x.model.lens[:] = [9, 5, 22]
+    assert x.model.fork([0, 0, 0]) == 0
+    x.table, x.held, x.lens = out
+    x.describe()
+    x.check(0)
+    start, count, status = x.lens.clone(), dev(np.array([1, 1, 0], np.int32)), torch.zeros_like(x.lens)
+    keep, src, dst = torch.zeros(3, 1, dtype=torch.int32, device="cuda"), dev(np.array([0], np.int32)), dev(np.array([19], np.int32))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ctx.kv_resize(x.c, start + 4, x.status)
+        ctx.kv_compact(x.c, start, keep, count, status)
+        ctx.kv_copy_pages(x.c, src, dst)
+    graph.replay()
+    assert x.model.resize([13, 13, 13]) == 0
+    x.model.compact([9, 9, 9], np.zeros((3, 1), np.int32), [1, 1, 0])
+    x.model.copy_pages([0], [19])
+    x.check(0)
+    assert status.tolist() == [0, 0, 0]
