@@ -816,9 +816,10 @@ cudaError_t launch_copy_pages(const KvView &c, const int32_t *src, const int32_t
 
 namespace {
 
-// Launches a kernel that hands out pages: its CTAs are one cluster, or one CTA.
+// Launches a kernel that hands out pages, with `words` words of shared memory a
+// slot: its CTAs are one cluster, or one CTA.
 template <class... Args>
-cudaError_t launch_plan(void (*many)(Args...), void (*one)(Args...), const KvView &c, size_t smem, bool pdl,
+cudaError_t launch_plan(void (*many)(Args...), void (*one)(Args...), const KvView &c, size_t words, bool pdl,
                         cudaStream_t stream, Args... args)
 {
     const bool cluster = c.pages > kClusterPages;
@@ -826,11 +827,13 @@ cudaError_t launch_plan(void (*many)(Args...), void (*one)(Args...), const KvVie
     cudaError_t e = cudaSuccess;
     if (cluster)
         e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && smem > 40 * 1024)  // beside the static shared memory
-        e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
     if (e != cudaSuccess)
         return e;
+    // Once a kernel and device, for the most slots there may be: a limit set to
+    // each call's own size could fall between another thread's check and launch.
+    if (resident_ctas((const void *)kernel, kPlanThreads, TB_KV_MAX_SLOTS * words * sizeof(int)) < 1)
+        return cudaErrorInvalidConfiguration;
+    const size_t smem = c.slots * words * sizeof(int);
     const int ctas = cluster ? kCluster : 1;
     return launch(kernel, dim3(ctas), kPlanThreads, smem, ctas, pdl, stream, args...);
 }
@@ -840,15 +843,15 @@ cudaError_t launch_plan(void (*many)(Args...), void (*one)(Args...), const KvVie
 cudaError_t launch_kv_resize(const KvView &c, const int32_t *capacity, int32_t *status, bool pdl,
                              cudaStream_t stream)
 {
-    return launch_plan(k_kv_resize<true>, k_kv_resize<false>, c, 3 * c.slots * sizeof(int), pdl, stream, c, capacity, status);
+    return launch_plan(k_kv_resize<true>, k_kv_resize<false>, c, 3, pdl, stream, c, capacity, status);
 }
 
 cudaError_t launch_kv_fork(const KvView &c, const int32_t *parents, int32_t *table_out,
                            int32_t *held_out, int32_t *lens_out, int32_t *status, bool pdl,
                            cudaStream_t stream)
 {
-    const cudaError_t e = launch_plan(k_fork_plan<true>, k_fork_plan<false>, c, 2 * c.slots * sizeof(int),
-                                      pdl, stream, c, parents, table_out, status);
+    const cudaError_t e = launch_plan(k_fork_plan<true>, k_fork_plan<false>, c, 2, pdl, stream, c, parents,
+                                      table_out, status);
     if (e != cudaSuccess)
         return e;
     const int per_row = (c.width + kPageThreads - 1) / kPageThreads, rows = c.slots * per_row;

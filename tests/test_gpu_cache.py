@@ -1,5 +1,7 @@
 """The page operations of the paged cache against a plain model: every bit of
 the pools, the table, the counts and the lengths has to be the model's."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -515,3 +517,31 @@ def test_calls_run_on_the_current_stream(ctx):
     x.model.copy_pages([0], [19])
     x.check(0)
     assert status.tolist() == [0, 0, 0]
+
+
+def test_threads_with_caches_of_different_sizes(ctx):
+    """Two threads, a context and a stream each: the shared memory that one's calls
+    need must not be taken from the other's."""
+    failed = []
+
+    def work(slots, calls):
+        try:
+            stream = torch.cuda.Stream()
+            with tb.Context(0) as own:
+                x = Cache(layers=1, heads=1, dim=8, slots=slots, width=1, pages=16, P=1)
+                capacity, parents = dev(np.zeros(slots, np.int32)), dev(np.full(slots, -1, np.int32))
+                out = [torch.empty_like(t) for t in (x.table, x.held, x.lens)]
+                torch.cuda.synchronize()
+                for _ in range(calls):
+                    own.kv_resize(x.c, capacity, x.status, stream)
+                    own.kv_fork(x.c, parents, *out, x.status, stream)
+                stream.synchronize()
+        except Exception as e:  # told to the test below
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(slots, 4000)) for slots in (8192, 4000, 5200, 7000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
