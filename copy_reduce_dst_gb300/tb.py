@@ -660,7 +660,9 @@ class Context:
                  "tb_kv_copy_pages")
 
     def kv_resize(self, cache: KvCache, capacity, status, stream=None):
-        """tb_kv_resize: each slot gets exactly the pages of capacity[s] tokens."""
+        """tb_kv_resize: each slot gets exactly the pages of capacity[s] tokens;
+        status: 0, pages missing, or -1 (past the table's width, or a cut inside
+        a page that other slots share)."""
         self._ok(lib.tb_kv_resize(self._h, cache.ref, _int32(capacity, "capacity", cache.per_slot),
                                   _int32(status, "status", (1,)), self._stream(stream)),
                  "tb_kv_resize")
@@ -676,7 +678,8 @@ class Context:
                  "tb_kv_fork")
 
     def kv_compact(self, cache: KvCache, start, keep, count, status, stream=None):
-        """tb_kv_compact: token start[s] + keep[s, i] moves to start[s] + i."""
+        """tb_kv_compact: token start[s] + keep[s, i] moves to start[s] + i;
+        status per slot: 0, 1 (pages shared with other slots), 2 (a bad list)."""
         slots, width = cache.per_slot, keep.shape[-1]
         self._ok(lib.tb_kv_compact(self._h, cache.ref, _int32(start, "start", slots),
                                    _int32(keep, "keep", slots + (width,)), width,

@@ -613,7 +613,11 @@ int tb_kv_copy_pages(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *src,
    in slot order, then row order, the lowest free one first, among those free
    when the call began: the result does not depend on timing.  *status
    (device) receives 0, the number of pages missing, or -1 when a capacity
-   needs more than table_width pages; unless it is 0 nothing else changes. */
+   needs more than table_width pages, or cuts a slot's tokens inside a page that
+   other rows share (the tokens after the cut would be written into it: cut at
+   the end of the page before, take a page with a second call and copy the
+   tokens there with tb_kv_copy_pages); unless it is 0 nothing else changes, in
+   no slot. */
 int tb_kv_resize(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *capacity,
                  int32_t *status, tb_stream stream);
 
@@ -644,10 +648,11 @@ int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
    the slot (tb_kv_resize gives them back).  A negative count leaves its slot
    alone.  Pools that share an element are refused: a token's place is written
    while others are read, once for each pool.  status[s] (device [slots])
-   receives 0; 1 when a token would move
-   into a page that other rows share; 2 when the list does not ascend, count
-   exceeds keep_stride or a position lies outside the slot's pages; a slot
-   with a nonzero status is unchanged. */
+   receives 0; 1 when other rows share a page that would be written now or by
+   later tokens: one from that of the first token that moves on, or, where none
+   moves (a mere cut), from that of the new end on; 2 when the list does not
+   ascend, count exceeds keep_stride or a position lies outside the slot's
+   pages; a slot with a nonzero status is unchanged. */
 int tb_kv_compact(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *start,
                   const int32_t *keep, int32_t keep_stride, const int32_t *count,
                   int32_t *status, tb_stream stream);

@@ -545,3 +545,27 @@ def test_threads_with_caches_of_different_sizes(ctx):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_statuses_of_cuts_in_shared_pages(ctx):
+    """A cut inside a shared page: the whole resize is refused with -1, a compaction
+    that moves nothing with 1, the other slots' growth and moves apart.  Then what
+    the header says to do about it."""
+    x = Cache(slots=3, width=5, pages=20, P=4)
+    x.resize(ctx, [9, 0, 4])
+    x.set_lens([9, 0, 4])
+    assert x.fork(ctx, [0, 0, 2]) == 0
+    assert x.resize(ctx, [6, -1, 12]) == -1
+    x.check(-1)
+    x.compact(ctx, [6, 0, 1], [[0], [0], [2]], [0, -1, 1])
+    x.check()
+    assert x.lens.tolist() == [9, 9, 2]
+    page = int(x.table[0, 1])  # two of its tokens are to stay
+    assert x.resize(ctx, [4, -1, 12]) == 0
+    assert x.resize(ctx, [6, -1, -1]) == 0
+    own = int(x.table[0, 1])
+    assert own != page
+    ctx.kv_copy_pages(x.c, dev(np.array([page], np.int32)), x.table[0, 1:2], tokens=dev(np.array([2], np.int32)))
+    x.model.copy_pages([page], [own], [2])
+    x.set_lens([6, 9, 2])
+    x.check(0)
