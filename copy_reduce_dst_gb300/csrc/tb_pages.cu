@@ -871,9 +871,13 @@ cudaError_t launch_compact(const KvView &c, const int32_t *start, const int32_t 
     // lists of 8 tokens 5.3 and 6.8 us, of 64 6.7 and 7.8, of 256 11.0 and 11.9;
     // 256 CTAs, of 128 10.4 and 10.6, of 256 16.6 and 15.1; 512, of 64 10.9 and
     // 10.7, of 128 15.5 and 13.8; 1024, of 8 9.8 and 9.8, of 64 17.1 and 15.0.
-    const bool check = keep_stride <= 256 && (int64_t)grid.x * grid.y * keep_stride <= 32768;
+    // (Eight warps take lists of 512 entries and more only.)
+    const bool check = WARPS < 8 && keep_stride <= 256 && (int64_t)grid.x * grid.y * keep_stride <= 32768;
     void (*kernel)(KvView, const int32_t *, const int32_t *, int32_t, const int32_t *, int32_t *) =
-        check ? k_kv_compact<true, WARPS, RING> : k_kv_compact<false, WARPS, RING>;
+        k_kv_compact<false, WARPS, RING>;
+    if constexpr (WARPS < 8)
+        if (check)
+            kernel = k_kv_compact<true, WARPS, RING>;
     constexpr int bytes = WARPS * sizeof(Moving<RING>);
     if (resident_ctas((const void *)kernel, 32 * WARPS, bytes) < 1)  // once a kernel and device; allows the memory
         return cudaErrorInvalidConfiguration;
