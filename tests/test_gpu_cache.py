@@ -569,3 +569,66 @@ def test_statuses_of_cuts_in_shared_pages(ctx):
     x.model.copy_pages([page], [own], [2])
     x.set_lens([6, 9, 2])
     x.check(0)
+
+
+@pytest.mark.parametrize("slots,layers,n", [(2, 1, 300), (2, 1, 257), (3, 8, 511), (40, 8, 140), (150, 8, 100),
+                                            (150, 8, 31), (2, 1, 512)])
+def test_compact_lists_of_every_length(ctx, slots, layers, n):
+    """Every form of the moving kernel: one, four and eight warps, with the lists
+    looked through by each of its CTAs or by a launch before."""
+    P, span = 8, n + n // 3 + 9
+    width = -(-(span + 20) // P)
+    x = Cache(layers=layers, slots=slots, width=width, pages=slots * width, P=P, heads=2, dim=64, seed=n)
+    x.resize(ctx, [width * P] * slots)
+    x.set_lens([span + 20] * slots)
+    g = np.random.default_rng(n)
+    keep = np.sort([g.permutation(span)[:n] for _ in range(slots)], axis=1)
+    keep[1, n // 2] = keep[1, n // 2 - 1]  # does not ascend
+    count = g.integers(n // 2, n + 1, slots)
+    count[1] = n
+    x.compact(ctx, g.integers(0, 21, slots).tolist(), keep, count.tolist())
+    x.check()
+
+
+def test_resize_of_a_pool_of_millions_of_pages(ctx):
+    """More pages than the hand-out keeps in registers (4096 a warp, 512 warps): the
+    free ones beyond are looked for again."""
+    pages, slots, width = 3000001, 600, 40
+    g = np.random.default_rng(29)
+    refs = np.ones(pages, np.int32)
+    refs[g.choice(pages, 20000, replace=False)] = 0
+    share = pages // 512
+    refs[200 * share + 4096:201 * share] = 0  # a run past the 4096th page of a warp's share
+    free = np.flatnonzero(refs == 0)
+    table, held, lens = dev(np.full((slots, width), -1, np.int32)), dev(np.zeros(slots, np.int32)), dev(np.zeros(slots, np.int32))
+    counts, status = dev(refs), dev(np.full(1, -7, np.int32))
+    c = tb.kv_cache(None, None, table, held, lens, counts, page_tokens=4)
+    need = g.integers(20, width + 1, slots)
+    ctx.kv_resize(c, dev((4 * need).astype(np.int32)), status)
+    torch.cuda.synchronize()
+    total = int(need.sum())
+    assert int(status) == 0 and 10000 < total < free.size
+    want = np.full((slots, width), -1, np.int32)
+    want[np.arange(width) < need[:, None]] = free[:total]
+    np.testing.assert_array_equal(table.cpu().numpy(), want)
+    np.testing.assert_array_equal(held.cpu().numpy(), need)
+    refs[free[:total]] = 1
+    np.testing.assert_array_equal(counts.cpu().numpy(), refs)
+    # Nearly all of the rest, then all given back.
+    rest = free.size - total
+    grow = need.copy()
+    for s in range(slots):
+        more = min(width - int(need[s]), rest - 1)
+        grow[s], rest = grow[s] + more, rest - more
+    ctx.kv_resize(c, dev((4 * grow).astype(np.int32)), status)
+    torch.cuda.synchronize()
+    left = int((counts == 0).sum())
+    assert int(status) == 0 and left == free.size - int(grow.sum())
+    order = np.concatenate([np.arange(need[s], grow[s]) + s * width for s in range(slots)])
+    np.testing.assert_array_equal(table.cpu().numpy().ravel()[order], free[total:total + order.size])
+    ctx.kv_resize(c, dev(np.zeros(slots, np.int32)), status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and int((counts == 0).sum()) == free.size and bool((table == -1).all())
+    want = np.ones(pages, np.int32)
+    want[free] = 0
+    np.testing.assert_array_equal(counts.cpu().numpy(), want)
