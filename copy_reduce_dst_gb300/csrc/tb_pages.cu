@@ -150,9 +150,10 @@ __device__ __forceinline__ int pages_for(int tokens, int page_tokens)
 // (their SMs read together; totals meet in distributed shared memory, so no
 // scratch memory is needed), and each warp counts, then hands out, a run of
 // them: 32 neighbouring pages a lane, as bits of a word kept in a register from
-// the first pass to the second.  Bound by the chain of its steps, not by its
-// bytes (512 slots x 4096 entries, 8.4 MB of counts: 24 us a call; with one CTA
-// 1670, a page a lane and every count read twice 65).
+// the first pass to the second.  A small call is bound by the chain of its steps (6
+// us); a large one by the work of 16 SMs on the counts, entries and pages given
+// back (512 slots, 1.17 million pages, 4.7 MB of counts, 109,000 entries: 24
+// us a call; with one CTA 1670, a page a lane and every count read twice 65).
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 16;
 // Pools of more pages than this are looked through by the cluster, others by one

@@ -42,8 +42,8 @@ using namespace dev;
 // HBM (8 sequences of 32768 positions, 32 rows: 174 us, 6.2 TB/s; 32 sequences
 // of up to 4096, 128 rows: 63 us, 4.3 TB/s; 40 us of that at the copy rate, 6 for
 // the join, the rest start and uneven ends of the runs); above, each stream's chain of scores,
-// maximum, weights and sums (131072 positions, 512 rows in two streams: 244 us,
-// 1130 TFLOP/s, tensor pipe 46% busy); for small calls the two launches and one
+// maximum, weights and sums (131072 positions, 512 rows in two streams: 238 us,
+// 1155 TFLOP/s, tensor pipe 50% busy); for small calls the two launches and one
 // tile's chain (500 positions, 32 rows: 11 us).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;       // positions of a tile
@@ -617,9 +617,13 @@ __device__ void load_role(const TreePlan &p, const Cta &cta, Walk walk)
 }
 
 // ---------------------------------------------------------------------------
-// Matrix products: one thread.  Scores over weights: the products of one thread
-// run in the order in which it issues them, so the next scores come after the
-// sums that read the weights in their place.
+// Matrix products: one thread.  The next scores are written where the weights
+// are that the sums issued before them read, with no wait between the two.  What
+// this relies on: the tensor core runs the products that one thread issues one
+// after another.  The PTX manual promises that order for products of one
+// accumulator and shape; these have two.  No weight has been seen overwritten
+// (results repeat bit for bit); a wait would cost the products' and the commit's
+// latency once a tile.
 // ---------------------------------------------------------------------------
 template <class S>
 __device__ void product_role(const TreePlan &p, const Cta &cta, Walk walk)

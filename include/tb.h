@@ -631,7 +631,9 @@ int tb_kv_resize(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *capacity,
    it goes on, else the lowest one; each other child takes a fresh page (in
    slot order, the lowest free one first, among those free when the call
    began) and the part-filled page's tokens are copied there in every layer.
-   Rows of childless slots are given back.  *status (device) receives 0, the
+   Rows of childless slots are given back.  Counts and tails change in one call,
+   so *cache has to describe all layers, at one stride: where each layer has
+   pools of its own that are not evenly spaced, a fork cannot serve them.  *status (device) receives 0, the
    number of pages missing, or -1 when a parent is >= slots; unless it is 0 the
    outputs are copies of the inputs and nothing else changes. */
 int tb_kv_fork(tb_ctx *ctx, const tb_kv_cache *cache, const int32_t *parents,
