@@ -693,8 +693,8 @@ typedef struct {
    not reach the result, whatever their bits.  Sums, maxima and the output
    accumulate in 32 bits; the weights exp(s_j - m) meet the values rounded to
    the cache's type (bf16: within 2^-9 of each; f16: within 2^-12 of each or
-   2^-32 of the row's largest, so that an infinite value under a weight below
-   2^-33 of the largest may come out as NaN).  The result depends on the inputs alone: two calls
+   2^-32 of the row's largest, so that an infinite value under a weight of
+   2^-32 of the largest or less may come out as NaN).  The result depends on the inputs alone: two calls
    give the same bits.  Every position needs a page in the slot's row; what
    has none reads as zeros.
    Limits (TB_ENOTSUP past them): rows * q_heads up to 2^30, and the calls that
